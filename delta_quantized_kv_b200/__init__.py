@@ -57,6 +57,22 @@ class dkv_cache(ctypes.Structure):
                 ("page_groups", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
 
 
+class dkv_kv4_desc(ctypes.Structure):
+    _fields_ = [("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class dkv_kv4_pool(ctypes.Structure):
+    _fields_ = [("desc", dkv_kv4_desc), ("base", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_bytes", ctypes.c_size_t), ("status", ctypes.c_void_p)]
+
+
+class dkv_kv4_batch(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("starts", ctypes.c_void_p)]
+
+
 _lib = None
 EXPORTS = ["dkv_abi_version", "dkv_cache_bytes", "dkv_cache_init", "dkv_encode", "dkv_append",
            "dkv_decode_workspace_bytes", "dkv_decode_attn", "dkv_decode_attn_split",
@@ -66,7 +82,9 @@ EXPORTS = ["dkv_abi_version", "dkv_cache_bytes", "dkv_cache_init", "dkv_encode",
            "dkv_cache_init_paged", "dkv_decode_workspace_bytes_mq", "dkv_decode_attn_mq",
            "dkv_append_decode_attn", "dkv_append_decode_attn_split",
            "dkv_append_decode_attn_merge", "dkv_lr_encode", "dkv_lr_decode_workspace_bytes",
-           "dkv_lr_decode_attn", "dkv_debug_division_check"]
+           "dkv_lr_decode_attn", "dkv_debug_division_check", "dkv_kv4_page_bytes",
+           "dkv_kv4_init", "dkv_kv4_append", "dkv_kv4_read", "dkv_kv4_decode_workspace_bytes",
+           "dkv_kv4_decode_attn"]
 
 
 def load():
@@ -84,6 +102,8 @@ def load():
     P, S, I, F = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_float
     PC = ctypes.POINTER(dkv_cache)
     PD = ctypes.POINTER(dkv_cache_desc)
+    L = ctypes.c_int64
+    P4, B4, D4 = (ctypes.POINTER(t) for t in (dkv_kv4_pool, dkv_kv4_batch, dkv_kv4_desc))
     sig = {
         "dkv_abi_version": ([], I),
         "dkv_cache_bytes": ([PD], S),
@@ -113,6 +133,12 @@ def load():
         "dkv_debug_division_check": ([P, I, P, P], I),
         "dkv_lr_decode_attn": ([ctypes.POINTER(dkv_lr_tensor), ctypes.POINTER(dkv_lr_tensor),
                                 I, I, I, I, I, P, P, I, I, F, P, P, S, P], I),
+        "dkv_kv4_page_bytes": ([D4], S),
+        "dkv_kv4_init": ([D4, P, L, P, P4, P], I),
+        "dkv_kv4_append": ([P4, B4, P, P, I, I, L, L, L, L, P], I),
+        "dkv_kv4_read": ([P4, B4, P, P, I, I, P], I),
+        "dkv_kv4_decode_workspace_bytes": ([D4, I, I, I, I], S),
+        "dkv_kv4_decode_attn": ([P4, B4, P, I, I, I, L, L, F, I, P, P, P, S, P], I),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -362,6 +388,46 @@ def dkv_debug_division_check(u, mismatches, stream=None) -> None:
                                            _stream(stream)), "dkv_debug_division_check")
 
 
+def dkv_kv4_page_bytes(desc: dkv_kv4_desc) -> int:
+    return load().dkv_kv4_page_bytes(ctypes.byref(desc))
+
+
+def dkv_kv4_init(desc: dkv_kv4_desc, pool, n_pages: int, status, stream=None) -> dkv_kv4_pool:
+    out = dkv_kv4_pool()
+    _check(load().dkv_kv4_init(ctypes.byref(desc), _ptr(pool), n_pages, _ptr(status),
+                               ctypes.byref(out), _stream(stream)), "dkv_kv4_init")
+    return out
+
+
+def dkv_kv4_append(pool: dkv_kv4_pool, seqs: dkv_kv4_batch, K, V, dtype, n_rows, k_row_stride,
+                   k_head_stride, v_row_stride, v_head_stride, stream=None) -> None:
+    _check(load().dkv_kv4_append(ctypes.byref(pool), ctypes.byref(seqs), _ptr(K), _ptr(V), dtype,
+                                 n_rows, k_row_stride, k_head_stride, v_row_stride,
+                                 v_head_stride, _stream(stream)), "dkv_kv4_append")
+
+
+def dkv_kv4_read(pool: dkv_kv4_pool, seqs: dkv_kv4_batch, K_out, V_out, dtype, n_rows,
+                 stream=None) -> None:
+    _check(load().dkv_kv4_read(ctypes.byref(pool), ctypes.byref(seqs), _ptr(K_out), _ptr(V_out),
+                               dtype, n_rows, _stream(stream)), "dkv_kv4_read")
+
+
+def dkv_kv4_decode_workspace_bytes(desc: dkv_kv4_desc, batch: int, max_pages: int,
+                                   n_q_heads: int, n_queries: int) -> int:
+    return load().dkv_kv4_decode_workspace_bytes(ctypes.byref(desc), batch, max_pages, n_q_heads,
+                                                 n_queries)
+
+
+def dkv_kv4_decode_attn(pool: dkv_kv4_pool, seqs: dkv_kv4_batch, Q, q_dtype, n_q_heads, n_queries,
+                        q_row_stride, q_head_stride, softmax_scale, window, out, lse, workspace,
+                        ws_bytes, stream=None) -> None:
+    _check(load().dkv_kv4_decode_attn(ctypes.byref(pool), ctypes.byref(seqs), _ptr(Q), q_dtype,
+                                      n_q_heads, n_queries, q_row_stride, q_head_stride,
+                                      softmax_scale, window, _ptr(out), _ptr(lse),
+                                      _ptr(workspace), ws_bytes, _stream(stream)),
+           "dkv_kv4_decode_attn")
+
+
 def dkv_get_device_status(cache: dkv_cache, stream=None) -> int:
     word = ctypes.c_int32(0)
     s = load().dkv_get_device_status(ctypes.byref(cache), ctypes.byref(word), _stream(stream))
@@ -528,3 +594,178 @@ class Cache:
 
     def device_status(self, stream=None) -> int:
         return dkv_get_device_status(self.c, stream)
+
+
+class Kv4Cache:
+    """A paged 4-bit cache (dkv_kv4_*) in torch-allocated device memory.
+
+    The pages hold keys and values in 4 bits, `group` channels a block; the
+    caller owns the block table (device int32 [batch, max_pages]), the lengths
+    (device int32 [batch], the call's own tokens included) and, for ragged
+    calls, the first row of each sequence (`starts`, device int32 [batch + 1];
+    None: the same number of rows for each).  Row i of a sequence's n rows
+    stands for position seq_len - n + i.  Every call launches on `stream`
+    (default: the current stream of the cache's device) and takes its scratch
+    and outputs from torch's allocator on that stream, so calls may be captured
+    into graphs and run on several streams at once.
+    """
+
+    def __init__(self, n_pages, n_kv_heads, head_dim=128, page_size=64, group=32, device="cuda",
+                 stream=None):
+        import torch
+        self.desc = dkv_kv4_desc(n_kv_heads, head_dim, group, page_size)
+        pb = dkv_kv4_page_bytes(self.desc)
+        if pb == 0 or n_pages < 1:
+            raise DkvError(DKV_EINVAL, "dkv_kv4_page_bytes")
+        self.device = torch.device(device)
+        if self.device.type != "cuda":
+            raise ValueError("a Kv4Cache lives on a CUDA device")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.pool = torch.empty(n_pages * pb + 256, dtype=torch.uint8, device=self.device)
+        self.status = torch.empty(1, dtype=torch.int32, device=self.device)
+        base = (self.pool.data_ptr() + 255) // 256 * 256
+        with torch.cuda.device(self.device):
+            self.c = dkv_kv4_init(self.desc, base, n_pages, self.status, stream)
+
+    # -- argument checks ----------------------------------------------------
+    def _tensor(self, x, name, dims=None):
+        if x.device != self.device:
+            raise ValueError(f"{name} is on {x.device}, the cache on {self.device}")
+        if dims is not None and x.dim() != dims:
+            raise ValueError(f"{name} has {x.dim()} dimensions, not {dims}")
+        return x
+
+    def _batch(self, block_table, seq_lens, starts):
+        import torch
+        for x, name, dims in ((block_table, "block_table", 2), (seq_lens, "seq_lens", 1),
+                              (starts, "starts", 1)):
+            if x is None and name == "starts":
+                continue
+            self._tensor(x, name, dims)
+            if x.dtype != torch.int32 or not x.is_contiguous():
+                raise ValueError(f"{name} must be contiguous int32")
+        B = seq_lens.shape[0]
+        if block_table.shape[0] != B or (starts is not None and starts.shape[0] != B + 1):
+            raise ValueError("block_table, seq_lens and starts disagree about the batch")
+        return dkv_kv4_batch(B, block_table.shape[1], block_table.data_ptr(),
+                             seq_lens.data_ptr(), None if starts is None else starts.data_ptr())
+
+    def _rows(self, x, name, heads=None):
+        """[rows, heads, head_dim] with contiguous channels."""
+        import torch
+        self._tensor(x, name, 3)
+        if x.shape[2] != self.desc.head_dim or (heads is not None and x.shape[1] != heads):
+            raise ValueError(f"{name} has shape {tuple(x.shape)}")
+        if x.stride(2) != 1:
+            raise ValueError(f"{name} must have contiguous channels")
+        if x.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+            raise ValueError(f"{name} is {x.dtype}")
+        return x
+
+    @staticmethod
+    def _strides(x):
+        """Row and head strides; a dimension of one has none that matters."""
+        return (x.stride(0) if x.shape[0] > 1 else 0, x.stride(1) if x.shape[1] > 1 else 0)
+
+    def _on(self, stream):
+        """Context in which allocations and launches belong to `stream` on the
+        cache's device, and its handle."""
+        import contextlib
+        import torch
+        if stream is not None and not isinstance(stream, int):
+            return torch.cuda.stream(stream), stream.cuda_stream
+        if stream is None:
+            handle = torch.cuda.current_stream(self.device).cuda_stream
+        else:
+            handle = stream
+            return torch.cuda.stream(torch.cuda.ExternalStream(stream, self.device)), handle
+        if torch.cuda.current_device() == self.device.index:
+            return contextlib.nullcontext(), handle
+        return torch.cuda.device(self.device), handle
+
+    # -- the operators ------------------------------------------------------
+    def append(self, K_new, V_new, block_table, seq_lens, starts=None, stream=None):
+        """Quantise the rows K_new, V_new [rows, n_kv_heads, head_dim] (fp32,
+        fp16 or bf16; views with row and head strides) into their sequences'
+        pages (dkv_kv4_append)."""
+        H = self.desc.n_kv_heads
+        self._rows(K_new, "K_new", H)
+        self._rows(V_new, "V_new", H)
+        if K_new.shape != V_new.shape or K_new.dtype != V_new.dtype:
+            raise ValueError("K_new and V_new differ in shape or dtype")
+        seqs = self._batch(block_table, seq_lens, starts)
+        if K_new.shape[0] == 0:
+            return
+        ctx, handle = self._on(stream)
+        with ctx:
+            dkv_kv4_append(self.c, seqs, K_new, V_new, _dtype_code(K_new.dtype), K_new.shape[0],
+                           *self._strides(K_new), *self._strides(V_new), handle)
+
+    def read(self, n_rows, block_table, seq_lens, starts=None, dtype=None, out=None, stream=None):
+        """The values held at the rows' positions (dkv_kv4_read): (K, V), each
+        [n_rows, n_kv_heads, head_dim] of dtype (default fp16).  out: a pair of
+        contiguous tensors to write instead; padding rows are left as they are."""
+        import torch
+        shape = (n_rows, self.desc.n_kv_heads, self.desc.head_dim)
+        seqs = self._batch(block_table, seq_lens, starts)
+        ctx, handle = self._on(stream)
+        with ctx:
+            if out is None:
+                dtype = torch.float16 if dtype is None else dtype
+                out = tuple(torch.empty(shape, dtype=dtype, device=self.device) for _ in range(2))
+            for x in out:
+                self._tensor(x, "out")
+                if tuple(x.shape) != shape or not x.is_contiguous() or x.dtype != out[0].dtype \
+                        or (dtype is not None and x.dtype != dtype):
+                    raise ValueError("out must be two contiguous tensors [n_rows, n_kv_heads, "
+                                     "head_dim] of dtype")
+            if n_rows:
+                dkv_kv4_read(self.c, seqs, out[0], out[1], _dtype_code(out[0].dtype), n_rows,
+                             handle)
+        return out
+
+    def _attn_out(self, Q, out, return_lse):
+        import torch
+        if out is None:
+            out = torch.empty(Q.shape, dtype=Q.dtype, device=self.device)
+        elif out.shape != Q.shape or out.dtype != Q.dtype or not out.is_contiguous():
+            raise ValueError("out must be contiguous, of Q's shape and dtype")
+        self._tensor(out, "out")
+        lse = torch.empty(Q.shape[:-1], dtype=torch.float32, device=self.device) \
+            if return_lse else None
+        return out, lse
+
+    def decode_attn(self, Q, softmax_scale, block_table, seq_lens, window=0, out=None,
+                    return_lse=False, stream=None):
+        """Decode attention (dkv_kv4_decode_attn).  Q [batch, n_q_heads, D], or
+        [batch, n_queries, n_q_heads, D] for the n_queries newest positions;
+        fp16 or bf16.  Returns Q's shape and dtype (and the log-sum-exp, fp32)."""
+        import torch
+        if Q.dim() not in (3, 4):
+            raise ValueError("Q has shape [batch, n_q_heads, D] or [batch, n_queries, n_q_heads, D]")
+        nq = Q.shape[1] if Q.dim() == 4 else 1
+        seqs = self._batch(block_table, seq_lens, None)
+        if Q.shape[0] != seqs.batch:
+            raise ValueError("Q and seq_lens disagree about the batch")
+        Hq = Q.shape[-2]
+        ctx, handle = self._on(stream)
+        with ctx:
+            # one row stride: a copy only where the batch is no plain view
+            rows = self._rows(Q.reshape(-1, *Q.shape[-2:]), "Q")
+            out, lse = self._attn_out(Q, out, return_lse)
+            nb = load().dkv_kv4_decode_workspace_bytes(ctypes.byref(self.desc), seqs.batch,
+                                                       seqs.max_pages, Hq, nq)
+            ws = torch.empty(nb // 4 + 4, dtype=torch.float32, device=self.device)
+            dkv_kv4_decode_attn(self.c, seqs, rows, _dtype_code(Q.dtype), Hq, nq,
+                                *self._strides(rows), softmax_scale, window, out, lse, ws, nb, handle)
+        return (out, lse) if return_lse else out
+
+    def device_status(self, stream=None) -> int:
+        """Read and clear the pool's status word (synchronises)."""
+        ctx, _ = self._on(stream)
+        with ctx:
+            word = int(self.status.item())
+            if word:
+                self.status.zero_()
+        return word

@@ -38,7 +38,7 @@
  *    the cache; the kernel skips the affected work and returns.  Nothing
  *    traps and nothing waits without a bound.  Read and clear the word with
  *    dkv_get_device_status.
- *  - head_dim must be 128.  Query head h reads KV head h / (Hq / Hkv).
+ *  - head_dim must be 128 (dkv_kv4_*: 64 or 128).  Query head h reads KV head h / (Hq / Hkv).
  *  - Inputs must be finite and within the fp16 range.
  */
 #ifndef DKV_H
@@ -51,7 +51,7 @@
 extern "C" {
 #endif
 
-#define DKV_ABI_VERSION 3
+#define DKV_ABI_VERSION 4
 
 typedef enum {
     DKV_OK = 0,
@@ -319,6 +319,116 @@ dkv_status dkv_lr_decode_attn(const dkv_lr_tensor *K, const dkv_lr_tensor *V, in
                               const int32_t *lens_dev, const void *Q, int32_t q_dtype,
                               int32_t n_q_heads, float softmax_scale, float *out,
                               void *workspace, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Paged 4-bit cache (dkv_kv4_*): keys and values of the tokens themselves in
+ * 4 bits with a scale and a zero point per block, in pages that a serving
+ * engine hands out.  The engine keeps the block table and the lengths; the
+ * library keeps nothing between calls.
+ *
+ * Block rule.  A block is `group` (32 or 64) channels of one token, kv head
+ * and tensor.  In fp32, with x clamped to [-32768, 32768] and NaN taken as 0:
+ * hi = max(0, max x), lo = min(0, min x); r = (hi - lo) * RN(1/15); the scale
+ * s is r rounded up to 7 significant bits (below 2^-14: to a multiple of
+ * 2^-20); zero = min(15, rint(-lo / s)); code = clamp(rint(x / s) + zero, 0,
+ * 15), with IEEE divisions and ties to even; s = 0 gives code = zero = 0.  The
+ * value held is x^ = (code - zero) * s, exact in fp16, and |x^ - x| <= s/2 (up
+ * to the fp32 rounding of x / s; s = 0: |x| < 2^-146).  A token takes D/2 + 2 D/group bytes per
+ * tensor and kv head (D = 128: 72 B at group 32, 68 B at group 64).
+ *
+ * Conventions, besides those above:
+ *  - head_dim is 64 or 128, page_size a positive multiple of 16 up to 65536.
+ *  - The current device must be the one that owns the memory and the stream.
+ *  - Rows of queries, keys and values are given with a row stride and a head
+ *    stride in elements (views of one fused projection); channels are
+ *    contiguous.  Bases and strides must be multiples of 16 bytes.
+ *  - In a dkv_kv4_batch, starts[b] .. starts[b+1]-1 are the rows of sequence b
+ *    (starts NULL: n_rows / batch rows each); row i of the n_b rows stands for
+ *    position seq_lens[b] - n_b + i, so seq_lens counts the rows' own tokens.
+ *    Rows at or behind starts[batch] are padding: never read, never written.
+ *    A sequence may have no rows, and length 0.
+ *  - Faults found on the device set bits of the pool's status word.
+ *    DKV_DEV_BAD_SEQLEN: a length outside [0, max_pages * page_size], or a
+ *    sequence with more rows than positions (its rows are skipped: not stored,
+ *    outputs left as they were; dkv_kv4_decode_attn treats a bad length as 0);
+ *    starts that are negative or decrease (which of the rows are then taken is
+ *    not defined, but nothing outside the rows and the sequences' pages is
+ *    touched).  DKV_DEV_BAD_PAGE: a block-table entry outside [0, n_pages)
+ *    where a position is needed (its token is not stored or read, or not seen
+ *    by the queries).
+ *  - Sequences may share pages to read.  A page that a call writes must belong
+ *    to one sequence in that call: two rows on one position leave either
+ *    row's bytes.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    int32_t n_kv_heads;    /* 1 .. 4096 */
+    int32_t head_dim;      /* 64 or 128 */
+    int32_t group;         /* channels per block: 32 or 64 */
+    int32_t page_size;     /* positions per page, a multiple of 16 */
+} dkv_kv4_desc;
+
+/* A pool of pages in caller-owned device memory, filled by dkv_kv4_init. */
+typedef struct {
+    dkv_kv4_desc desc;
+    void *base;
+    int64_t n_pages;
+    size_t page_bytes;
+    int32_t *status;       /* device status word, caller-owned */
+} dkv_kv4_pool;
+
+/* The sequences of one call (device arrays, 4-byte aligned, caller-owned;
+ * entries may change between calls). */
+typedef struct {
+    int32_t batch;         /* 1 .. 16384 */
+    int32_t max_pages;     /* block-table width; max_pages * page_size <= 2^30 */
+    const int32_t *block_table;  /* [batch][max_pages]: page of positions i*page_size ... */
+    const int32_t *seq_lens;     /* [batch]: positions held, the call's rows included */
+    const int32_t *starts;       /* [batch + 1] first row of each sequence, or NULL */
+} dkv_kv4_batch;
+
+/* Bytes of one page (0 for an invalid descriptor). */
+size_t dkv_kv4_page_bytes(const dkv_kv4_desc *desc);
+
+/* A pool of n_pages pages at `pool` (256-byte aligned, n_pages *
+ * dkv_kv4_page_bytes) with its status word at `status` (4-byte aligned).
+ * Zeroes both with cudaMemsetAsync on `stream` (zeroed pages hold zeros). */
+dkv_status dkv_kv4_init(const dkv_kv4_desc *desc, void *pool, int64_t n_pages, int32_t *status,
+                        dkv_kv4_pool *out, void *stream);
+
+/* Quantise n_rows rows of keys and values, as they are written, into the pages
+ * of their sequences.  K, V: row i, kv head h at i * row_stride + h *
+ * head_stride elements of `dtype` (any of the three).  All inputs are taken
+ * (the block rule clamps; NaN becomes 0). */
+dkv_status dkv_kv4_append(const dkv_kv4_pool *pool, const dkv_kv4_batch *seqs, const void *K,
+                          const void *V, int32_t dtype, int32_t n_rows, int64_t k_row_stride,
+                          int64_t k_head_stride, int64_t v_row_stride, int64_t v_head_stride,
+                          void *stream);
+
+/* The values held at the rows' positions, as K_out, V_out [n_rows][n_kv_heads]
+ * [head_dim] of `dtype` (fp16 and fp32 hold them exactly, bf16 rounds once). */
+dkv_status dkv_kv4_read(const dkv_kv4_pool *pool, const dkv_kv4_batch *seqs, void *K_out,
+                        void *V_out, int32_t dtype, int32_t n_rows, void *stream);
+
+/* Decode attention over the pages: the n_queries newest positions of every
+ * sequence ask.  Query t of sequence b (row b * n_queries + t of Q) stands at
+ * position p = seq_lens[b] - n_queries + t and sees the positions max(0, p -
+ * window + 1) .. p (window 0: all up to p).  out = softmax(softmax_scale * q .
+ * k^) v^ in Q's dtype (fp16 or bf16), [batch * n_queries][n_q_heads][D]
+ * contiguous, not overlapping Q; lse (NULL: not written) fp32
+ * [batch * n_queries][n_q_heads], the natural log of the sum of exp(score).  A
+ * query that sees nothing gives zeros and -inf.  seqs->starts is not read.
+ * Query head h reads kv head h / (n_q_heads / n_kv_heads).  Scores, softmax
+ * statistics and sums are fp32; the weights are rounded to fp16 once.  1 <=
+ * n_queries <= 16.  DKV_F32 queries: DKV_EUNSUPPORTED.  Two launches.
+ * workspace: device scratch, 16-byte aligned, of >= the _workspace_bytes (for
+ * the current device), used by one call at a time. */
+size_t dkv_kv4_decode_workspace_bytes(const dkv_kv4_desc *desc, int32_t batch, int32_t max_pages,
+                                      int32_t n_q_heads, int32_t n_queries);
+dkv_status dkv_kv4_decode_attn(const dkv_kv4_pool *pool, const dkv_kv4_batch *seqs, const void *Q,
+                               int32_t q_dtype, int32_t n_q_heads, int32_t n_queries,
+                               int64_t q_row_stride, int64_t q_head_stride, float softmax_scale,
+                               int32_t window, void *out, float *lse, void *workspace,
+                               size_t ws_bytes, void *stream);
 
 /* Size of the library-owned scratch array used by dkv_decode_attn_noalloc. */
 #define DKV_NOALLOC_SCRATCH_BYTES (16u << 20)
