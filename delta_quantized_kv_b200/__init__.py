@@ -84,7 +84,7 @@ EXPORTS = ["dkv_abi_version", "dkv_cache_bytes", "dkv_cache_init", "dkv_encode",
            "dkv_append_decode_attn_merge", "dkv_lr_encode", "dkv_lr_decode_workspace_bytes",
            "dkv_lr_decode_attn", "dkv_debug_division_check", "dkv_kv4_page_bytes",
            "dkv_kv4_init", "dkv_kv4_append", "dkv_kv4_read", "dkv_kv4_decode_workspace_bytes",
-           "dkv_kv4_decode_attn"]
+           "dkv_kv4_decode_attn", "dkv_kv4_prompt_workspace_bytes", "dkv_kv4_prompt_attn"]
 
 
 def load():
@@ -138,6 +138,8 @@ def load():
         "dkv_kv4_append": ([P4, B4, P, P, I, I, L, L, L, L, P], I),
         "dkv_kv4_read": ([P4, B4, P, P, I, I, P], I),
         "dkv_kv4_decode_workspace_bytes": ([D4, I, I, I, I], S),
+        "dkv_kv4_prompt_workspace_bytes": ([D4, I, I, I, I, I], S),
+        "dkv_kv4_prompt_attn": ([P4, B4, P, I, I, I, L, L, F, I, P, P, P, S, P], I),
         "dkv_kv4_decode_attn": ([P4, B4, P, I, I, I, L, L, F, I, P, P, P, S, P], I),
     }
     for name, (args, res) in sig.items():
@@ -426,6 +428,22 @@ def dkv_kv4_decode_attn(pool: dkv_kv4_pool, seqs: dkv_kv4_batch, Q, q_dtype, n_q
                                       softmax_scale, window, _ptr(out), _ptr(lse),
                                       _ptr(workspace), ws_bytes, _stream(stream)),
            "dkv_kv4_decode_attn")
+
+
+def dkv_kv4_prompt_workspace_bytes(desc: dkv_kv4_desc, batch: int, max_pages: int,
+                                   n_q_heads: int, n_rows: int, ragged: bool) -> int:
+    return load().dkv_kv4_prompt_workspace_bytes(ctypes.byref(desc), batch, max_pages, n_q_heads,
+                                                 n_rows, int(ragged))
+
+
+def dkv_kv4_prompt_attn(pool: dkv_kv4_pool, seqs: dkv_kv4_batch, Q, q_dtype, n_q_heads, n_rows,
+                        q_row_stride, q_head_stride, softmax_scale, window, out, lse, workspace,
+                        ws_bytes, stream=None) -> None:
+    _check(load().dkv_kv4_prompt_attn(ctypes.byref(pool), ctypes.byref(seqs), _ptr(Q), q_dtype,
+                                      n_q_heads, n_rows, q_row_stride, q_head_stride,
+                                      softmax_scale, window, _ptr(out), _ptr(lse),
+                                      _ptr(workspace), ws_bytes, _stream(stream)),
+           "dkv_kv4_prompt_attn")
 
 
 def dkv_get_device_status(cache: dkv_cache, stream=None) -> int:
@@ -759,6 +777,29 @@ class Kv4Cache:
             ws = torch.empty(nb // 4 + 4, dtype=torch.float32, device=self.device)
             dkv_kv4_decode_attn(self.c, seqs, rows, _dtype_code(Q.dtype), Hq, nq,
                                 *self._strides(rows), softmax_scale, window, out, lse, ws, nb, handle)
+        return (out, lse) if return_lse else out
+
+    def prompt_attn(self, Q, softmax_scale, block_table, seq_lens, starts=None, window=0,
+                    out=None, return_lse=False, stream=None):
+        """Prompt attention (dkv_kv4_prompt_attn): Q [rows, n_q_heads, D] (fp16
+        or bf16), the rows of `starts`, whose keys and values are in the cache.
+        Returns Q's shape and dtype (and the log-sum-exp, fp32); padding rows
+        of `out` are left as they are (undefined in a new one)."""
+        import torch
+        self._rows(Q, "Q")
+        seqs = self._batch(block_table, seq_lens, starts)
+        n, Hq = Q.shape[:2]
+        ctx, handle = self._on(stream)
+        with ctx:
+            out, lse = self._attn_out(Q, out, return_lse)
+            if n:
+                nb = load().dkv_kv4_prompt_workspace_bytes(
+                    ctypes.byref(self.desc), seqs.batch, seqs.max_pages, Hq, n,
+                    starts is not None)
+                ws = torch.empty(nb // 4 + 4, dtype=torch.float32, device=self.device)
+                dkv_kv4_prompt_attn(self.c, seqs, Q, _dtype_code(Q.dtype), Hq, n,
+                                    *self._strides(Q), softmax_scale, window, out, lse, ws, nb,
+                                    handle)
         return (out, lse) if return_lse else out
 
     def device_status(self, stream=None) -> int:

@@ -22,6 +22,7 @@ inline bool valid_scale(float s) { return s > 0.f && s < 1e30f; }   // finite, >
 constexpr int32_t kMaxQueries = 16;
 constexpr int64_t kMaxPositions = (int64_t)1 << 30;
 constexpr int64_t kMaxRows = (int64_t)1 << 33;       // rows x kv heads: grids stay in range
+constexpr int64_t kMaxQueryRows = (int64_t)1 << 30;  // prompt: rows x query heads
 constexpr int64_t kMaxRuns = (int64_t)1 << 24;       // decode: batch x kv heads x head groups
 
 int64_t decode_runs(int32_t batch, int32_t H, int32_t Hq, int32_t nq) {
@@ -210,6 +211,49 @@ dkv_status dkv_kv4_decode_attn(const dkv_kv4_pool *pool, const dkv_kv4_batch *se
     if (ws_bytes < (size_t)need * sizeof(float)) return DKV_ECAPACITY;
     return cuda_status(dkv::kv4::launch_decode(v, pool->desc.head_dim, pool->desc.group, q,
                                                n_queries, static_cast<float *>(workspace), need,
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+size_t dkv_kv4_prompt_workspace_bytes(const dkv_kv4_desc *desc, int32_t batch, int32_t max_pages,
+                                      int32_t n_q_heads, int32_t n_rows, int32_t ragged) {
+    if (check_desc(desc) != DKV_OK || check_geometry(desc, batch, max_pages) != DKV_OK) return 0;
+    if (n_q_heads < 1 || n_q_heads % desc->n_kv_heads != 0 || n_rows < 1 ||
+        (int64_t)n_rows * n_q_heads > kMaxQueryRows || (!ragged && n_rows % batch != 0))
+        return 0;
+    View v;
+    std::memset(&v, 0, sizeof(v));
+    v.H = desc->n_kv_heads;
+    v.page_size = desc->page_size;
+    v.B = batch;
+    v.max_pages = max_pages;
+    v.n_rows = n_rows;
+    int64_t f = 0;
+    if (dkv::kv4::prompt_workspace_floats(v, desc->head_dim, n_q_heads, ragged != 0, &f) !=
+        cudaSuccess)
+        return 0;
+    return (size_t)f * sizeof(float);
+}
+
+dkv_status dkv_kv4_prompt_attn(const dkv_kv4_pool *pool, const dkv_kv4_batch *seqs, const void *Q,
+                               int32_t q_dtype, int32_t n_q_heads, int32_t n_rows,
+                               int64_t q_row_stride, int64_t q_head_stride, float softmax_scale,
+                               int32_t window, void *out, float *lse, void *workspace,
+                               size_t ws_bytes, void *stream) {
+    View v;
+    dkv_status s = make_view(pool, seqs, n_rows, true, &v);
+    if (s != DKV_OK) return s;
+    Query q;
+    s = check_query(v, Q, q_dtype, n_q_heads, q_row_stride, q_head_stride, softmax_scale, window,
+                    out, lse, workspace, &q);
+    if (s != DKV_OK) return s;
+    if ((int64_t)n_rows * n_q_heads > kMaxQueryRows) return DKV_ECAPACITY;
+    int64_t need = 0;
+    if (dkv::kv4::prompt_workspace_floats(v, pool->desc.head_dim, n_q_heads, v.starts != nullptr,
+                                          &need) != cudaSuccess)
+        return DKV_ECUDA;
+    if (ws_bytes < (size_t)need * sizeof(float)) return DKV_ECAPACITY;
+    return cuda_status(dkv::kv4::launch_prompt(v, pool->desc.head_dim, pool->desc.group, q,
+                                               static_cast<float *>(workspace), need,
                                                static_cast<cudaStream_t>(stream)));
 }
 

@@ -33,8 +33,8 @@ cudaError_t decode_workspace_floats(const View &v, int D, int Hq, int nq, int64_
 cudaError_t launch_decode(const View &v, int D, int G, const Query &q, int nq, float *ws,
                           int64_t ws_floats, cudaStream_t st);
 
-// Prompt: ragged query rows (v.starts, v.n_rows).
-cudaError_t prompt_workspace_floats(const View &v, int D, int Hq, int64_t *floats);
+// Prompt: ragged query rows (v.starts, v.n_rows), or the same number each.
+cudaError_t prompt_workspace_floats(const View &v, int D, int Hq, bool ragged, int64_t *floats);
 cudaError_t launch_prompt(const View &v, int D, int G, const Query &q, float *ws,
                           int64_t ws_floats, cudaStream_t st);
 

@@ -430,6 +430,24 @@ dkv_status dkv_kv4_decode_attn(const dkv_kv4_pool *pool, const dkv_kv4_batch *se
                                int32_t window, void *out, float *lse, void *workspace,
                                size_t ws_bytes, void *stream);
 
+/* Prompt attention over the pages: ragged chunks of queries, n_rows in all,
+ * in the rows that seqs->starts gives each sequence (the chunk's own keys and
+ * values already appended; a chunk may be of any length, one row too).  The
+ * query of position p sees the positions max(0, p - window + 1) .. p (window
+ * 0: all up to p).  Arguments, formula, types and precision as for
+ * dkv_kv4_decode_attn, with out [n_rows][n_q_heads][D] and lse
+ * [n_rows][n_q_heads].  A sequence whose starts pass n_rows is skipped too
+ * (DKV_DEV_BAD_SEQLEN).  n_rows * n_q_heads <= 2^30.  One launch, or two when
+ * the rows are few and the table is long (the positions are then split, and
+ * the parts joined). */
+size_t dkv_kv4_prompt_workspace_bytes(const dkv_kv4_desc *desc, int32_t batch, int32_t max_pages,
+                                      int32_t n_q_heads, int32_t n_rows, int32_t ragged);
+dkv_status dkv_kv4_prompt_attn(const dkv_kv4_pool *pool, const dkv_kv4_batch *seqs, const void *Q,
+                               int32_t q_dtype, int32_t n_q_heads, int32_t n_rows,
+                               int64_t q_row_stride, int64_t q_head_stride, float softmax_scale,
+                               int32_t window, void *out, float *lse, void *workspace,
+                               size_t ws_bytes, void *stream);
+
 /* Size of the library-owned scratch array used by dkv_decode_attn_noalloc. */
 #define DKV_NOALLOC_SCRATCH_BYTES (16u << 20)
 
