@@ -37,7 +37,7 @@ namespace {
 
 constexpr int TM = 128;            // query rows per tile
 constexpr int TN = 128;            // positions per tile
-constexpr int THREADS = 512;
+constexpr int THREADS = 640;
 constexpr int STAGES = 2;
 
 struct Prompt {
@@ -60,9 +60,10 @@ struct Smem {
     static constexpr int BYTES = (END > 120 * 1024 ? END : 120 * 1024) + 1024;
 };
 
-// barriers, in 8-byte slots
-enum { KFULL = 0, KFREE = 2, VFULL = 4, VFREE = 6, SFULL = 8, PFULL = 10, OFULL = 12, DRAIN = 14,
-       N_BAR = 15 };
+// barriers, in 8-byte slots; PFULL: the first and the second half of a tile's
+// weights, for each query tile
+enum { KFULL = 0, KFREE = 2, VFULL = 4, VFREE = 6, SFULL = 8, PFULL = 10, OFULL = 14, DRAIN = 16,
+       N_BAR = 17 };
 
 // ---- tcgen05 ---------------------------------------------------------------
 __device__ inline void tm_alloc(uint32_t dst_smem, uint32_t cols) {
@@ -74,18 +75,24 @@ __device__ inline void tm_alloc(uint32_t dst_smem, uint32_t cols) {
 __device__ inline void tm_free(uint32_t addr, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(addr), "r"(cols));
 }
-__device__ inline void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// Descriptors come as their low words (the address, and the leading offset);
+// HI is the high word.  The k-th step of an operand is a constant further on.
+template <uint32_t HI_A, uint32_t HI_B, uint32_t IDESC>
+__device__ inline void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.u32 p, %3, 0;\n"
+        " mov.b64 da, {%1, %4};\n mov.b64 db, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %6, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(acc), "n"(HI_A), "n"(HI_B), "n"(IDESC)
         : "memory");
 }
-__device__ inline void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+template <uint32_t HI_B, uint32_t IDESC>
+__device__ inline void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.u32 p, %3, 0;\n"
+        " mov.b64 db, {%2, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %5, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(acc), "n"(HI_B), "n"(IDESC)
         : "memory");
 }
 __device__ inline void tm_commit(uint64_t *bar) {
@@ -99,6 +106,14 @@ __device__ inline void tm_fence_before() {
 }
 __device__ inline void tm_fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+}
+#define DKV_RW8(r, i) \
+    "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), \
+        "+r"(r[i + 6]), "+r"(r[i + 7])
+// Waits for this warp's loads; what uses r comes after.
+__device__ inline void tm_wait_ld32(uint32_t *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : DKV_RW8(r, 0), DKV_RW8(r, 8), DKV_RW8(r, 16), DKV_RW8(r, 24)::"memory");
 }
 __device__ inline void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 __device__ inline void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
@@ -137,8 +152,8 @@ __device__ inline void tm_st16(uint32_t addr, const uint32_t *r) {
 __device__ inline bool warp_wait(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
 }
-// Registers of this warpgroup.  512 threads are launched with 128 each; 2 x 184
-// + 96 + 40 <= 4 x 128.
+// Registers of this warpgroup.  640 threads are launched with 96 each; 2 x 152
+// + 2 x 64 + 48 = 5 x 96.
 template <int N>
 __device__ inline void regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
@@ -151,22 +166,67 @@ __device__ inline void regs_down() {
 __device__ inline void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
 }
+// One arrival for the warp, behind what all its lanes did.
+__device__ inline void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
 
 // Instruction descriptor, kind::f16: fp16 A and B, fp32 D, A K-major.
 __device__ constexpr uint32_t idesc(int m, int n, bool b_mn) {
     return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(m >> 4) << 24);
 }
-// Shared-memory descriptor, 128-byte swizzle: leading and stride byte offsets.
-__device__ inline uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
-           (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// Shared-memory descriptor, 128-byte swizzle: low word from the address and the
+// leading offset, high word from the stride offset (all in bytes).
+__device__ inline uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+    return ((addr >> 4) & 0x3FFFu) | (lbo >> 4) << 16;
+}
+__device__ constexpr uint32_t desc_hi(uint32_t sbo) { return sbo >> 4 | 1u << 14 | 2u << 29; }
+__device__ inline bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
 }
 
 __device__ inline float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Two fp32 operations in one instruction.
+__device__ inline uint64_t f2(float lo, float hi) {
+    return (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+}
+__device__ inline float f2_lo(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ inline float f2_hi(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ inline uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ inline uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// 2^x of two x on the FMA pipes (-126 <= x < 127, finite; below, 2^-126): x = n
+// + f with |f| <= 1/2 by adding 1.5 * 2^23, and 2^f by the degree-5 polynomial
+// of least relative error with p(0) = 1.  Error 1.6e-7, below ex2.approx's.
+__device__ inline uint64_t ex2_poly(uint64_t x) {
+    x = f2(fmaxf(f2_lo(x), -126.f), fmaxf(f2_hi(x), -126.f));
+    const uint64_t t = add2(x, f2(12582912.f, 12582912.f));
+    const uint64_t n = add2(t, f2(-12582912.f, -12582912.f));
+    const uint64_t f = fma2(n, f2(-1.f, -1.f), x);
+    uint64_t y = f2(0x1.5bba14p-10f, 0x1.5bba14p-10f);
+    y = fma2(y, f, f2(0x1.3cea88p-7f, 0x1.3cea88p-7f));
+    y = fma2(y, f, f2(0x1.c6b752p-5f, 0x1.c6b752p-5f));
+    y = fma2(y, f, f2(0x1.ebf9bcp-3f, 0x1.ebf9bcp-3f));
+    y = fma2(y, f, f2(0x1.62e42ap-1f, 0x1.62e42ap-1f));
+    y = fma2(y, f, f2(1.f, 1.f));
+    return (uint64_t)((uint32_t)(y >> 32) + ((uint32_t)(t >> 32) << 23)) << 32 |
+           (uint64_t)((uint32_t)y + ((uint32_t)t << 23));
 }
 
 // Exponent e with max |q| 2^e in [2^14, 2^15).
@@ -280,6 +340,50 @@ __device__ inline Meta meta_of(uint32_t m) {       // one block's halfword
     return r;
 }
 
+// Bits below n.
+__device__ inline uint32_t below(int n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+}
+
+// Scores that the row does not see.
+__device__ inline void hide(uint32_t (&s)[32], uint32_t see) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+        if (!(see >> k & 1)) s[k] = 0xFF800000u;
+}
+__device__ inline float max32(const uint32_t (&s)[32]) {
+    float a = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+    float b = fmaxf(__uint_as_float(s[2]), __uint_as_float(s[3]));
+#pragma unroll
+    for (int k = 4; k < 32; k += 4) {
+        a = fmaxf(fmaxf(a, __uint_as_float(s[k])), __uint_as_float(s[k + 1]));
+        b = fmaxf(fmaxf(b, __uint_as_float(s[k + 2])), __uint_as_float(s[k + 3]));
+    }
+    return fmaxf(a, b);
+}
+
+// 32 of a row's scores to weights 2^(c s + r), as fp16 and into the sum.  NP of
+// the 16 pairs go by the polynomial, the others by ex2.approx: that unit gives
+// 16 results a clock and SM, 2048 clocks for the CTA's two tiles, as long as
+// the tensor cores take.
+constexpr int POLY = 4;
+template <int NP>
+__device__ inline void weights(const uint32_t (&s)[32], uint64_t c2, uint64_t r2,
+                               uint32_t (&w)[16], uint64_t &l2) {
+    uint64_t la = l2, lb = 0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const uint64_t x = fma2((uint64_t)s[2 * k + 1] << 32 | s[2 * k], c2, r2);
+        uint64_t y;
+        if (NP > 0 && (k * NP) % 16 < NP) y = ex2_poly(x);
+        else y = f2(ex2(f2_lo(x)), ex2(f2_hi(x)));
+        if (k & 1) lb = add2(lb, y);
+        else la = add2(la, y);
+        w[k] = pack_h2(f2_lo(y), f2_hi(y));
+    }
+    l2 = add2(la, lb);
+}
+
 template <typename L, int DT>
 __global__ void __launch_bounds__(THREADS, 1)
 prompt_kernel(View v, Prompt p) {
@@ -299,14 +403,15 @@ prompt_kernel(View v, Prompt p) {
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(bars + KFULL + i, 128);
+            mbar_init(bars + KFULL + i, 4);
             mbar_init(bars + KFREE + i, 1);
-            mbar_init(bars + VFULL + i, 128);
+            mbar_init(bars + VFULL + i, 4);
             mbar_init(bars + VFREE + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bars + SFULL + i, 1);
-            mbar_init(bars + PFULL + i, 128);
+            mbar_init(bars + PFULL + 2 * i, 4);
+            mbar_init(bars + PFULL + 2 * i + 1, 4);
             mbar_init(bars + OFULL + i, 1);
         }
         mbar_init(bars + DRAIN, 1);
@@ -317,7 +422,7 @@ prompt_kernel(View v, Prompt p) {
     Job job;
     if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) check_starts(v);
     if (!find_job(v, p, blockIdx.x, blockIdx.y, &job)) return;    // all warps agree
-    if (warp == 12) tm_alloc(smem_u32(tm_slot), 512);
+    if (warp == 16) tm_alloc(smem_u32(tm_slot), 512);
     tm_fence_before();
     __syncthreads();
     tm_fence_after();
@@ -327,7 +432,7 @@ prompt_kernel(View v, Prompt p) {
 
     if (wg < 2) {
         // ---------------- softmax ------------------------------------------
-        regs_up<184>();
+        regs_up<152>();
         const int qi = wg;
         const int row = job.row0 + qi * TM + tid;
         const bool have = row < job.nrow;
@@ -380,7 +485,8 @@ prompt_kernel(View v, Prompt p) {
         asm volatile("bar.sync 1, 288;\n" ::: "memory");       // 8 softmax warps + the MMA warp
         const uint32_t lane_base = (uint32_t)(warp & 3) << 21;
         const uint32_t tS = tm + lane_base + qi * 128, tO = tm + lane_base + 256 + qi * L::D;
-        float ref = 0.f, l = 0.f;
+        float ref = 0.f;
+        uint64_t l2 = 0;                   // the sum, in two halves
         bool any = false;                  // ref has been set
         const int row_first = job.row0 + qi * TM;
         const int pmin = job.pos0 + row_first / p.G;     // the tile's first and last positions
@@ -389,25 +495,39 @@ prompt_kernel(View v, Prompt p) {
             for (int j = 0; j < ntile; ++j) {
                 if (!warp_wait(bars + SFULL + qi, j & 1)) { ok = false; break; }
                 tm_fence_after();
-                uint32_t s[128];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tm_ld32(s + 32 * i, tS + 32 * i);
-                tm_wait_ld();
+                // all scores are looked at for the maximum, then the second half is
+                // loaded again: 128 of them do not stay in registers
+                uint32_t s0[32], s1[32];
                 const int kv = job.kv0 + j * TN;
                 const uint32_t vm = valid[j & 3];
-                if (kv + TN - 1 > pmin || (p.q.window > 0 && kv <= pmax - p.q.window) ||
-                    vm != ALL) {
-#pragma unroll
-                    for (int i = 0; i < 128; ++i) {
-                        const int at = kv + i;
-                        if (at > pos || at <= lo || !(vm >> (i / 32 * 8 + i / RT % 2) & 1)) s[i] = 0xFF800000u;
+                const bool edge = kv + TN - 1 > pmin ||
+                                  (p.q.window > 0 && kv <= pmax - p.q.window) || vm != ALL;
+                // (the row sees (lo, pos], and records that are there)
+                auto see = [&](int i) {
+                    const int at = kv + 32 * i;
+                    const uint32_t v2 = vm >> (8 * i);
+                    return below(pos + 1 - at) & ~below(lo + 1 - at) &
+                           ((v2 & 1 ? 0xFFFFu : 0u) | (v2 & 2 ? 0xFFFF0000u : 0u));
+                };
+                float mx;
+                {
+                    uint32_t s2[32], s3[32];
+                    tm_ld32(s0, tS);
+                    tm_ld32(s1, tS + 32);
+                    tm_ld32(s2, tS + 64);
+                    tm_ld32(s3, tS + 96);
+                    tm_wait_ld32(s0);
+                    tm_wait_ld32(s1);
+                    tm_wait_ld32(s2);
+                    tm_wait_ld32(s3);
+                    if (edge) {
+                        hide(s0, see(0));
+                        hide(s1, see(1));
+                        hide(s2, see(2));
+                        hide(s3, see(3));
                     }
+                    mx = fmaxf(fmaxf(max32(s0), max32(s1)), fmaxf(max32(s2), max32(s3))) * c1;
                 }
-                float mx = __uint_as_float(s[0]);
-#pragma unroll
-                for (int i = 1; i < 127; i += 2)
-                    mx = fmaxf(fmaxf(mx, __uint_as_float(s[i])), __uint_as_float(s[i + 1]));
-                mx = fmaxf(mx, __uint_as_float(s[127])) * c1;
                 // (NaN scores leave mx to the others; their weights are NaN)
                 const bool up = mx > -INFINITY && (!any || mx > ref + 15.f);
                 if (__any_sync(0xffffffffu, up)) {
@@ -430,27 +550,39 @@ prompt_kernel(View v, Prompt p) {
                         }
                     }
                     if (up) {
-                        l *= f;
+                        l2 = fma2(l2, f2(f, f), 0);
                         ref = nref;
                         any = true;
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float a = ex2(fmaf(__uint_as_float(s[32 * i + 2 * k]), c1, -ref));
-                        const float b = ex2(fmaf(__uint_as_float(s[32 * i + 2 * k + 1]), c1, -ref));
-                        l += a + b;
-                        w[k] = pack_h2(a, b);
-                    }
+                // the polynomial takes finite scores only
+                const uint64_t c2 = f2(c1, c1), r2 = f2(-ref, -ref);
+                const bool plain = edge || !__all_sync(0xffffffffu, fabsf(mx) < INFINITY);
+                uint32_t w[16];
+                auto put = [&](int i, uint32_t (&s)[32]) {
+                    if (plain) weights<0>(s, c2, r2, w, l2);
+                    else weights<POLY>(s, c2, r2, w, l2);
                     tm_st16(tS + 16 * i, w);
+                    if (i & 1) {
+                        tm_wait_st();
+                        tm_fence_before();
+                        warp_arrive(bars + PFULL + 2 * qi + (i >> 1));
+                    }
+                };
+                put(0, s0);
+                tm_ld32(s0, tS + 64);
+                put(1, s1);
+                tm_ld32(s1, tS + 96);
+                tm_wait_ld32(s0);
+                tm_wait_ld32(s1);
+                if (edge) {
+                    hide(s0, see(2));
+                    hide(s1, see(3));
                 }
-                tm_wait_st();
-                tm_fence_before();
-                mbar_arrive(bars + PFULL + qi);
+                put(2, s0);
+                put(3, s1);
             }
+            const float l = f2_lo(l2) + f2_hi(l2);
             // ---------------- output ---------------------------------------
             if (ok && ntile > 0) ok = warp_wait(bars + OFULL + qi, (ntile - 1) & 1);
             if (!ok) set_status(v.status, DKV_DEV_TIMEOUT);
@@ -515,12 +647,16 @@ prompt_kernel(View v, Prompt p) {
                 }
             }
         }
-    } else if (wg == 2) {
-        regs_down<96>();
-        // ---------------- dequantisation -----------------------------------
+    } else if (wg < 4) {
+        // ---------------- dequantisation: K (2), V (3) ---------------------
+        regs_down<64>();
         bool ok = true;
-        uint32_t kw[L::D / 8], vw[L::D / 8], km[L::NB], vmeta[L::NB];
-        const uint32_t sw = (uint32_t)tid * 128u;
+        const bool isk = wg == 2;
+        uint64_t *full = bars + (isk ? KFULL : VFULL), *free_ = bars + (isk ? KFREE : VFREE);
+        uint32_t cw[L::D / 8], cm[L::NB], nw[L::D / 8], nm[L::NB];
+        bool here = false;
+        // position `at`'s words; false where the record is missing below the
+        // length (a bad page): it is not seen
         auto fetch = [&](int j) {
             const int at = job.kv0 + j * TN + tid;
             const uint8_t *rec = at < job.len ? record(v, job.b, job.kvh, at, L::REC) : nullptr;
@@ -528,59 +664,52 @@ prompt_kernel(View v, Prompt p) {
                 rec = nullptr;
             const int t = at & (RT - 1);
 #pragma unroll
-            for (int i = 0; i < L::D / 8; ++i) kw[i] = vw[i] = 0u;
+            for (int i = 0; i < L::D / 8; ++i) nw[i] = 0u;
 #pragma unroll
-            for (int i = 0; i < L::NB; ++i) km[i] = vmeta[i] = 0u;
+            for (int i = 0; i < L::NB; ++i) nm[i] = 0u;
             if (rec) {
-                const uint4 *a = reinterpret_cast<const uint4 *>(rec + L::k_word(t, 0));
-                const uint4 *b = reinterpret_cast<const uint4 *>(rec + L::OFF_V + t * L::ROW);
+                const uint4 *a = reinterpret_cast<const uint4 *>(
+                    rec + (isk ? L::k_word(t, 0) : L::OFF_V + t * L::ROW));
 #pragma unroll
                 for (int i = 0; i < L::D / 32; ++i) {
-                    const uint4 x = a[i], y = b[i];
-                    kw[4 * i] = x.x; kw[4 * i + 1] = x.y; kw[4 * i + 2] = x.z; kw[4 * i + 3] = x.w;
-                    vw[4 * i] = y.x; vw[4 * i + 1] = y.y; vw[4 * i + 2] = y.z; vw[4 * i + 3] = y.w;
+                    const uint4 x = a[i];
+                    nw[4 * i] = x.x; nw[4 * i + 1] = x.y; nw[4 * i + 2] = x.z; nw[4 * i + 3] = x.w;
                 }
 #pragma unroll
-                for (int i = 0; i < L::NB; ++i) {
-                    km[i] = *reinterpret_cast<const uint16_t *>(rec + L::k_meta(t, i));
-                    vmeta[i] = *reinterpret_cast<const uint16_t *>(rec + L::v_meta(t, i));
-                }
+                for (int i = 0; i < L::NB; ++i)
+                    nm[i] = *reinterpret_cast<const uint16_t *>(
+                        rec + (isk ? L::k_meta(t, i) : L::v_meta(t, i)));
             }
-            // a record that is missing below the length (a bad page) is not seen
-            return (unsigned)__ballot_sync(0xffffffffu, rec != nullptr || at >= job.len);
+            here = rec != nullptr || at >= job.len;
         };
-        unsigned there = ntile > 0 ? fetch(0) : 0u;
+        if (ntile > 0) fetch(0);
         for (int j = 0; j < ntile; ++j) {
             const int st = j % STAGES, ph = (j / STAGES) & 1;
-            // K
-            if (j >= STAGES && !warp_wait(bars + KFREE + st, ph ^ 1)) { ok = false; break; }
-            if (lane == 0)          // two records a warp: lanes 0..15 and 16..31
-                reinterpret_cast<volatile uint8_t *>(valid + (j & 3))[warp & 3] =
-                    (uint8_t)(((there & 0xFFFFu) == 0xFFFFu ? 1 : 0) |
-                              ((there >> 16) == 0xFFFFu ? 2 : 0));
-            {
-                uint8_t *dst = smem + S::K + st * S::TILE + sw;
-                Meta m[L::NB];
 #pragma unroll
-                for (int i = 0; i < L::NB; ++i) m[i] = meta_of(km[i]);
+            for (int i = 0; i < L::D / 8; ++i) cw[i] = nw[i];
+#pragma unroll
+            for (int i = 0; i < L::NB; ++i) cm[i] = nm[i];
+            const unsigned there = __ballot_sync(0xffffffffu, here);
+            if (j + 1 < ntile) fetch(j + 1);
+            if (j >= STAGES && !warp_wait(free_ + st, ph ^ 1)) { ok = false; break; }
+            Meta m[L::NB];
+#pragma unroll
+            for (int i = 0; i < L::NB; ++i) m[i] = meta_of(cm[i]);
+            uint8_t *dst = smem + (isk ? S::K : S::V) + st * S::TILE + tid * 128;
+            if (isk) {
+                if (lane == 0)          // two records a warp: lanes 0..15 and 16..31
+                    reinterpret_cast<volatile uint8_t *>(valid + (j & 3))[warp & 3] =
+                        (uint8_t)(((there & 0xFFFFu) == 0xFFFFu ? 1 : 0) |
+                                  ((there >> 16) == 0xFFFFu ? 2 : 0));
 #pragma unroll
                 for (int w = 0; w < L::D / 8; ++w) {
                     const int c8 = 4 * (w % L::NJ) + w / L::NJ;       // word t * NJ + j
                     const Meta &q = m[c8 * 8 / L::G];
                     *reinterpret_cast<uint4 *>(dst + (c8 >> 3) * (128 * 128) +
                                                (((c8 & 7) ^ (tid & 7)) << 4)) =
-                        dequant8(kw[w], q.s, q.z1024, q.z64);
+                        dequant8(cw[w], q.s, q.z1024, q.z64);
                 }
-                fence_proxy_async();
-                mbar_arrive(bars + KFULL + st);
-            }
-            // V
-            if (j >= STAGES && !warp_wait(bars + VFREE + st, ph ^ 1)) { ok = false; break; }
-            {
-                uint8_t *dst = smem + S::V + st * S::TILE + sw;
-                Meta m[L::NB];
-#pragma unroll
-                for (int i = 0; i < L::NB; ++i) m[i] = meta_of(vmeta[i]);
+            } else {
                 const int t = (job.kv0 + j * TN + tid) & (RT - 1);
                 const int flip = L::D == 128 ? ((t >> 1) & 1) << 2 : 0;
 #pragma unroll
@@ -592,69 +721,87 @@ prompt_kernel(View v, Prompt p) {
                     const int g = c ^ flip;
                     uint4 y;
                     if constexpr (L::G == 64) {
-                        y = dequant8(vw[w], m[u].s, m[u].z1024, m[u].z64);
+                        y = dequant8(cw[w], m[u].s, m[u].z1024, m[u].z64);
                     } else {
                         // low halves are nibbles 0-3, high halves 4-7
                         const Meta &a = m[2 * u], &b = m[2 * u + 1];
-                        y = dequant8(vw[w], __lows2half2(a.s, b.s), __lows2half2(a.z1024, b.z1024),
+                        y = dequant8(cw[w], __lows2half2(a.s, b.s), __lows2half2(a.z1024, b.z1024),
                                      __lows2half2(a.z64, b.z64));
                     }
                     *reinterpret_cast<uint4 *>(dst + u * (128 * 128) +
                                                ((g ^ (tid & 7)) << 4)) = y;
                 }
-                fence_proxy_async();
-                mbar_arrive(bars + VFULL + st);
             }
-            if (j + 1 < ntile) there = fetch(j + 1);
+            fence_proxy_async();
+            warp_arrive(full + st);
         }
         if (!ok) set_status(v.status, DKV_DEV_TIMEOUT);
     } else {
         // ---------------- MMA ----------------------------------------------
-        regs_down<40>();
-        if (warp == 12) {
-        asm volatile("bar.sync 1, 288;\n" ::: "memory");
-        if (lane == 0) {
+        // the warp walks in step, one thread of it issues: everything the
+        // instructions take is the same in all lanes
+        regs_down<48>();
+        if (warp == 16) {
+            asm volatile("bar.sync 1, 288;\n" ::: "memory");
             bool ok = true;
-            const uint32_t q0 = smem_u32(smem + S::Q), k0 = smem_u32(smem + S::K),
-                           v0 = smem_u32(smem + S::V);
             constexpr uint32_t IS = idesc(TM, TN, false), IO = idesc(TM, L::D, true);
+            constexpr uint32_t HI = desc_hi(1024);
+            const bool leader = elect_one();
+            const uint32_t q0 = desc_lo(smem_u32(smem + S::Q), 16),
+                           k0 = desc_lo(smem_u32(smem + S::K), 16),
+                           v0 = desc_lo(smem_u32(smem + S::V), 128 * 128);
             auto scores = [&](int qi, int st) {
+                const uint32_t a = q0 + qi * (S::TILE >> 4), b = k0 + st * (S::TILE >> 4);
+                if (leader) {
 #pragma unroll
-                for (int k = 0; k < L::D / 16; ++k) {
-                    const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32;
-                    mma_ss(tm + qi * 128, sdesc(q0 + qi * S::TILE + off, 16, 1024),
-                           sdesc(k0 + st * S::TILE + off, 16, 1024), IS, k > 0);
+                    for (int k = 0; k < L::D / 16; ++k) {
+                        const uint32_t off = (k >> 2) * (128 * 128 >> 4) + (k & 3) * (32 >> 4);
+                        mma_ss<HI, HI, IS>(tm + qi * 128, a + off, b + off, k > 0);
+                    }
+                    tm_commit(bars + SFULL + qi);
                 }
-                tm_commit(bars + SFULL + qi);
+                __syncwarp();
             };
-            auto values = [&](int qi, int st, bool acc) {
+            auto values = [&](int qi, int st, int half, bool acc) {
+                const uint32_t a = tm + qi * 128 + half * (TN / 4);
+                const uint32_t b = v0 + (st * S::TILE + half * (TN / 32) * 2048 >> 4);
+                if (leader) {
 #pragma unroll
-                for (int k = 0; k < TN / 16; ++k)
-                    mma_ts(tm + 256 + qi * L::D, tm + qi * 128 + k * 8,
-                           sdesc(v0 + st * S::TILE + k * 2048, 128 * 128, 1024), IO, acc || k > 0);
-                tm_commit(bars + OFULL + qi);
+                    for (int k = 0; k < TN / 32; ++k)
+                        mma_ts<HI, IO>(tm + 256 + qi * L::D, a + k * 8, b + k * (2048 >> 4),
+                                       acc || k > 0);
+                    if (half) tm_commit(bars + OFULL + qi);
+                }
+                __syncwarp();
+            };
+            auto commit = [&](uint64_t *bar) {
+                if (leader) tm_commit(bar);
+                __syncwarp();
             };
             if (ntile > 0) {
-                ok = mbar_wait_bounded(bars + KFULL, 0);
+                ok = warp_wait(bars + KFULL, 0);
                 tm_fence_after();
                 if (ok) {
                     for (int qi = 0; qi < qtiles; ++qi) scores(qi, 0);
-                    tm_commit(bars + KFREE);
+                    commit(bars + KFREE);
                 }
             }
             for (int j = 0; ok && j < ntile; ++j) {
                 const int st = j % STAGES, ph = (j / STAGES) & 1;
                 const int sn = (j + 1) % STAGES, pn = ((j + 1) / STAGES) & 1;
-                ok = mbar_wait_bounded(bars + VFULL + st, ph);
+                ok = warp_wait(bars + VFULL + st, ph);
                 if (!ok) break;
                 for (int qi = 0; qi < qtiles; ++qi) {
-                    ok = mbar_wait_bounded(bars + PFULL + qi, j & 1);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        ok = ok && warp_wait(bars + PFULL + 2 * qi + half, j & 1);
+                        tm_fence_after();
+                        if (ok) values(qi, st, half, j > 0 || half > 0);
+                    }
                     if (!ok) break;
-                    tm_fence_after();
-                    values(qi, st, j > 0);
                     if (j + 1 < ntile) {
                         if (qi == 0) {
-                            ok = mbar_wait_bounded(bars + KFULL + sn, pn);
+                            ok = warp_wait(bars + KFULL + sn, pn);
                             if (!ok) break;
                             tm_fence_after();
                         }
@@ -662,20 +809,18 @@ prompt_kernel(View v, Prompt p) {
                     }
                 }
                 if (!ok) break;
-                tm_commit(bars + VFREE + st);
-                if (j + 1 < ntile) tm_commit(bars + KFREE + sn);
+                commit(bars + VFREE + st);
+                if (j + 1 < ntile) commit(bars + KFREE + sn);
             }
             if (!ok) set_status(v.status, DKV_DEV_TIMEOUT);
             // nothing is in flight when tensor memory is given back
-            tm_commit(bars + DRAIN);
-            mbar_wait_bounded(bars + DRAIN, 0);
-        }
-        __syncwarp();
+            commit(bars + DRAIN);
+            warp_wait(bars + DRAIN, 0);
         }
     }
     tm_fence_before();
     __syncthreads();
-    if (warp == 12) tm_free(tm, 512);
+    if (warp == 16) tm_free(tm, 512);
 }
 
 // Joins the splits of a row: one warp per (row, head).
