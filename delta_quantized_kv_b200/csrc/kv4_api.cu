@@ -228,7 +228,7 @@ size_t dkv_kv4_prompt_workspace_bytes(const dkv_kv4_desc *desc, int32_t batch, i
     v.max_pages = max_pages;
     v.n_rows = n_rows;
     int64_t f = 0;
-    if (dkv::kv4::prompt_workspace_floats(v, desc->head_dim, n_q_heads, ragged != 0, &f) !=
+    if (dkv::kv4::prompt_workspace_floats(v, desc->head_dim, n_q_heads, &f) !=
         cudaSuccess)
         return 0;
     return (size_t)f * sizeof(float);
@@ -248,8 +248,7 @@ dkv_status dkv_kv4_prompt_attn(const dkv_kv4_pool *pool, const dkv_kv4_batch *se
     if (s != DKV_OK) return s;
     if ((int64_t)n_rows * n_q_heads > kMaxQueryRows) return DKV_ECAPACITY;
     int64_t need = 0;
-    if (dkv::kv4::prompt_workspace_floats(v, pool->desc.head_dim, n_q_heads, v.starts != nullptr,
-                                          &need) != cudaSuccess)
+    if (dkv::kv4::prompt_workspace_floats(v, pool->desc.head_dim, n_q_heads, &need) != cudaSuccess)
         return DKV_ECUDA;
     if (ws_bytes < (size_t)need * sizeof(float)) return DKV_ECAPACITY;
     return cuda_status(dkv::kv4::launch_prompt(v, pool->desc.head_dim, pool->desc.group, q,

@@ -34,7 +34,7 @@ cudaError_t launch_decode(const View &v, int D, int G, const Query &q, int nq, f
                           int64_t ws_floats, cudaStream_t st);
 
 // Prompt: ragged query rows (v.starts, v.n_rows), or the same number each.
-cudaError_t prompt_workspace_floats(const View &v, int D, int Hq, bool ragged, int64_t *floats);
+cudaError_t prompt_workspace_floats(const View &v, int D, int Hq, int64_t *floats);
 cudaError_t launch_prompt(const View &v, int D, int G, const Query &q, float *ws,
                           int64_t ws_floats, cudaStream_t st);
 

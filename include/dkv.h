@@ -437,9 +437,8 @@ dkv_status dkv_kv4_decode_attn(const dkv_kv4_pool *pool, const dkv_kv4_batch *se
  * 0: all up to p).  Arguments, formula, types and precision as for
  * dkv_kv4_decode_attn, with out [n_rows][n_q_heads][D] and lse
  * [n_rows][n_q_heads].  A sequence whose starts pass n_rows is skipped too
- * (DKV_DEV_BAD_SEQLEN).  n_rows * n_q_heads <= 2^30.  One launch, or two when
- * the rows are few and the table is long (the positions are then split, and
- * the parts joined). */
+ * (DKV_DEV_BAD_SEQLEN).  n_rows * n_q_heads <= 2^30.  Two launches.  ragged:
+ * whether seqs->starts will be given. */
 size_t dkv_kv4_prompt_workspace_bytes(const dkv_kv4_desc *desc, int32_t batch, int32_t max_pages,
                                       int32_t n_q_heads, int32_t n_rows, int32_t ragged);
 dkv_status dkv_kv4_prompt_attn(const dkv_kv4_pool *pool, const dkv_kv4_batch *seqs, const void *Q,
