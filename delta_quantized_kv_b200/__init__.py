@@ -645,6 +645,12 @@ class Kv4Cache:
         base = (self.pool.data_ptr() + 255) // 256 * 256
         with torch.cuda.device(self.device):
             self.c = dkv_kv4_init(self.desc, base, n_pages, self.status, stream)
+        # what every call needs at hand: a decode step's calls take microseconds
+        self._torch, self._lib, self._index = torch, load(), self.device.index
+        self._desc, self._pool = ctypes.byref(self.desc), ctypes.byref(self.c)
+        self._codes = {torch.float32: DKV_F32, torch.float16: DKV_F16, torch.bfloat16: DKV_BF16}
+        self._stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
     # -- argument checks ----------------------------------------------------
     def _tensor(self, x, name, dims=None):
@@ -655,129 +661,144 @@ class Kv4Cache:
         return x
 
     def _batch(self, block_table, seq_lens, starts):
-        import torch
-        for x, name, dims in ((block_table, "block_table", 2), (seq_lens, "seq_lens", 1),
-                              (starts, "starts", 1)):
-            if x is None and name == "starts":
+        i32, dev = self._torch.int32, self._index
+        for x, dims in ((block_table, 2), (seq_lens, 1), (starts, 1)):
+            if x is None and x is starts:
                 continue
-            self._tensor(x, name, dims)
-            if x.dtype != torch.int32 or not x.is_contiguous():
+            if x.get_device() != dev or x.dim() != dims or x.dtype is not i32 \
+                    or not x.is_contiguous():
+                name = "block_table" if dims == 2 else "seq_lens" if x is seq_lens else "starts"
+                self._tensor(x, name, dims)
                 raise ValueError(f"{name} must be contiguous int32")
-        B = seq_lens.shape[0]
-        if block_table.shape[0] != B or (starts is not None and starts.shape[0] != B + 1):
+        B, (rows, width) = len(seq_lens), block_table.shape
+        if rows != B or (starts is not None and len(starts) != B + 1):
             raise ValueError("block_table, seq_lens and starts disagree about the batch")
-        return dkv_kv4_batch(B, block_table.shape[1], block_table.data_ptr(),
-                             seq_lens.data_ptr(), None if starts is None else starts.data_ptr())
+        return dkv_kv4_batch(B, width, block_table.data_ptr(), seq_lens.data_ptr(),
+                             None if starts is None else starts.data_ptr())
 
     def _rows(self, x, name, heads=None):
-        """[rows, heads, head_dim] with contiguous channels."""
-        import torch
-        self._tensor(x, name, 3)
-        if x.shape[2] != self.desc.head_dim or (heads is not None and x.shape[1] != heads):
-            raise ValueError(f"{name} has shape {tuple(x.shape)}")
-        if x.stride(2) != 1:
+        """[rows, heads, head_dim] with contiguous channels: shape, row and head
+        strides (a dimension of one has none that matters) and type code."""
+        if x.get_device() != self._index or x.dim() != 3:
+            self._tensor(x, name, 3)
+        shape, (row, head, one) = x.shape, x.stride()
+        if shape[2] != self.desc.head_dim or (heads is not None and shape[1] != heads):
+            raise ValueError(f"{name} has shape {tuple(shape)}")
+        if one != 1:
             raise ValueError(f"{name} must have contiguous channels")
-        if x.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        code = self._codes.get(x.dtype)
+        if code is None:
             raise ValueError(f"{name} is {x.dtype}")
-        return x
+        return shape, row if shape[0] > 1 else 0, head if shape[1] > 1 else 0, code
 
-    @staticmethod
-    def _strides(x):
-        """Row and head strides; a dimension of one has none that matters."""
-        return (x.stride(0) if x.shape[0] > 1 else 0, x.stride(1) if x.shape[1] > 1 else 0)
-
-    def _on(self, stream):
-        """Context in which allocations and launches belong to `stream` on the
-        cache's device, and its handle."""
-        import contextlib
-        import torch
-        if stream is not None and not isinstance(stream, int):
-            return torch.cuda.stream(stream), stream.cuda_stream
+    def _elsewhere(self, stream):
+        """None where calls go to the current stream of the current device;
+        otherwise a context that makes it so."""
+        torch = self._torch
         if stream is None:
-            handle = torch.cuda.current_stream(self.device).cuda_stream
-        else:
-            handle = stream
-            return torch.cuda.stream(torch.cuda.ExternalStream(stream, self.device)), handle
-        if torch.cuda.current_device() == self.device.index:
-            return contextlib.nullcontext(), handle
-        return torch.cuda.device(self.device), handle
+            if torch.cuda.current_device() == self._index:
+                return None
+            return torch.cuda.device(self.device)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, self.device)
+        return torch.cuda.stream(stream)
 
     # -- the operators ------------------------------------------------------
     def append(self, K_new, V_new, block_table, seq_lens, starts=None, stream=None):
         """Quantise the rows K_new, V_new [rows, n_kv_heads, head_dim] (fp32,
         fp16 or bf16; views with row and head strides) into their sequences'
         pages (dkv_kv4_append)."""
+        ctx = self._elsewhere(stream)
+        if ctx is not None:
+            with ctx:
+                return self.append(K_new, V_new, block_table, seq_lens, starts)
         H = self.desc.n_kv_heads
-        self._rows(K_new, "K_new", H)
-        self._rows(V_new, "V_new", H)
-        if K_new.shape != V_new.shape or K_new.dtype != V_new.dtype:
+        shape, k_row, k_head, code = self._rows(K_new, "K_new", H)
+        v_shape, v_row, v_head, v_code = self._rows(V_new, "V_new", H)
+        if shape != v_shape or code != v_code:
             raise ValueError("K_new and V_new differ in shape or dtype")
         seqs = self._batch(block_table, seq_lens, starts)
-        if K_new.shape[0] == 0:
-            return
-        ctx, handle = self._on(stream)
-        with ctx:
-            dkv_kv4_append(self.c, seqs, K_new, V_new, _dtype_code(K_new.dtype), K_new.shape[0],
-                           *self._strides(K_new), *self._strides(V_new), handle)
+        if shape[0]:
+            _check(self._lib.dkv_kv4_append(
+                self._pool, ctypes.byref(seqs), K_new.data_ptr(), V_new.data_ptr(), code, shape[0],
+                k_row, k_head, v_row, v_head, self._stream(self._index)), "dkv_kv4_append")
 
     def read(self, n_rows, block_table, seq_lens, starts=None, dtype=None, out=None, stream=None):
         """The values held at the rows' positions (dkv_kv4_read): (K, V), each
         [n_rows, n_kv_heads, head_dim] of dtype (default fp16).  out: a pair of
         contiguous tensors to write instead; padding rows are left as they are."""
-        import torch
+        ctx = self._elsewhere(stream)
+        if ctx is not None:
+            with ctx:
+                return self.read(n_rows, block_table, seq_lens, starts, dtype, out)
+        torch = self._torch
         shape = (n_rows, self.desc.n_kv_heads, self.desc.head_dim)
         seqs = self._batch(block_table, seq_lens, starts)
-        ctx, handle = self._on(stream)
-        with ctx:
-            if out is None:
-                dtype = torch.float16 if dtype is None else dtype
-                out = tuple(torch.empty(shape, dtype=dtype, device=self.device) for _ in range(2))
+        if out is None:
+            dtype = torch.float16 if dtype is None else dtype
+            out = (torch.empty(shape, dtype=dtype, device=self.device),
+                   torch.empty(shape, dtype=dtype, device=self.device))
+        else:
             for x in out:
                 self._tensor(x, "out")
                 if tuple(x.shape) != shape or not x.is_contiguous() or x.dtype != out[0].dtype \
                         or (dtype is not None and x.dtype != dtype):
                     raise ValueError("out must be two contiguous tensors [n_rows, n_kv_heads, "
                                      "head_dim] of dtype")
-            if n_rows:
-                dkv_kv4_read(self.c, seqs, out[0], out[1], _dtype_code(out[0].dtype), n_rows,
-                             handle)
+        k, v = out
+        if n_rows:
+            _check(self._lib.dkv_kv4_read(self._pool, ctypes.byref(seqs), k.data_ptr(),
+                                          v.data_ptr(), self._codes[k.dtype], n_rows,
+                                          self._stream(self._index)), "dkv_kv4_read")
         return out
 
-    def _attn_out(self, Q, out, return_lse):
-        import torch
+    def _attn(self, what, rows, Q, sizes, n_queries, seqs, softmax_scale, window, out, return_lse):
+        """The rest of an attention call.  rows: Q as [rows, n_q_heads, D];
+        sizes: what its workspace depends on."""
+        torch = self._torch
+        shape, row, head, code = self._rows(rows, "Q")
         if out is None:
             out = torch.empty(Q.shape, dtype=Q.dtype, device=self.device)
-        elif out.shape != Q.shape or out.dtype != Q.dtype or not out.is_contiguous():
-            raise ValueError("out must be contiguous, of Q's shape and dtype")
-        self._tensor(out, "out")
+        else:
+            if out.shape != Q.shape or out.dtype != Q.dtype or not out.is_contiguous():
+                raise ValueError("out must be contiguous, of Q's shape and dtype")
+            self._tensor(out, "out")
         lse = torch.empty(Q.shape[:-1], dtype=torch.float32, device=self.device) \
             if return_lse else None
-        return out, lse
+        if shape[0]:
+            lib = self._lib
+            size, call = (lib.dkv_kv4_decode_workspace_bytes, lib.dkv_kv4_decode_attn) \
+                if what == "decode" else (lib.dkv_kv4_prompt_workspace_bytes, lib.dkv_kv4_prompt_attn)
+            nb = size(self._desc, *sizes)
+            ws = torch.empty(nb + 16, dtype=torch.uint8, device=self.device)
+            _check(call(self._pool, ctypes.byref(seqs), rows.data_ptr(), code, shape[1], n_queries,
+                     row, head, softmax_scale, window, out.data_ptr(),
+                     None if lse is None else lse.data_ptr(), ws.data_ptr(), nb,
+                     self._stream(self._index)), f"dkv_kv4_{what}_attn")
+        return (out, lse) if return_lse else out
 
     def decode_attn(self, Q, softmax_scale, block_table, seq_lens, window=0, out=None,
                     return_lse=False, stream=None):
         """Decode attention (dkv_kv4_decode_attn).  Q [batch, n_q_heads, D], or
         [batch, n_queries, n_q_heads, D] for the n_queries newest positions;
         fp16 or bf16.  Returns Q's shape and dtype (and the log-sum-exp, fp32)."""
-        import torch
-        if Q.dim() not in (3, 4):
+        ctx = self._elsewhere(stream)
+        if ctx is not None:
+            with ctx:
+                return self.decode_attn(Q, softmax_scale, block_table, seq_lens, window, out,
+                                        return_lse)
+        shape = Q.shape
+        if len(shape) not in (3, 4):
             raise ValueError("Q has shape [batch, n_q_heads, D] or [batch, n_queries, n_q_heads, D]")
-        nq = Q.shape[1] if Q.dim() == 4 else 1
         seqs = self._batch(block_table, seq_lens, None)
-        if Q.shape[0] != seqs.batch:
+        if shape[0] != seqs.batch:
             raise ValueError("Q and seq_lens disagree about the batch")
-        Hq = Q.shape[-2]
-        ctx, handle = self._on(stream)
-        with ctx:
+        nq, rows = 1, Q
+        if len(shape) == 4:
             # one row stride: a copy only where the batch is no plain view
-            rows = self._rows(Q.reshape(-1, *Q.shape[-2:]), "Q")
-            out, lse = self._attn_out(Q, out, return_lse)
-            nb = load().dkv_kv4_decode_workspace_bytes(ctypes.byref(self.desc), seqs.batch,
-                                                       seqs.max_pages, Hq, nq)
-            ws = torch.empty(nb // 4 + 4, dtype=torch.float32, device=self.device)
-            dkv_kv4_decode_attn(self.c, seqs, rows, _dtype_code(Q.dtype), Hq, nq,
-                                *self._strides(rows), softmax_scale, window, out, lse, ws, nb, handle)
-        return (out, lse) if return_lse else out
+            nq, rows = shape[1], Q.reshape(-1, shape[2], shape[3])
+        return self._attn("decode", rows, Q, (seqs.batch, seqs.max_pages, shape[-2], nq), nq, seqs,
+                          softmax_scale, window, out, return_lse)
 
     def prompt_attn(self, Q, softmax_scale, block_table, seq_lens, starts=None, window=0,
                     out=None, return_lse=False, stream=None):
@@ -785,28 +806,25 @@ class Kv4Cache:
         or bf16), the rows of `starts`, whose keys and values are in the cache.
         Returns Q's shape and dtype (and the log-sum-exp, fp32); padding rows
         of `out` are left as they are (undefined in a new one)."""
-        import torch
-        self._rows(Q, "Q")
+        ctx = self._elsewhere(stream)
+        if ctx is not None:
+            with ctx:
+                return self.prompt_attn(Q, softmax_scale, block_table, seq_lens, starts, window,
+                                        out, return_lse)
+        if Q.dim() != 3:
+            self._tensor(Q, "Q", 3)
         seqs = self._batch(block_table, seq_lens, starts)
         n, Hq = Q.shape[:2]
-        ctx, handle = self._on(stream)
-        with ctx:
-            out, lse = self._attn_out(Q, out, return_lse)
-            if n:
-                nb = load().dkv_kv4_prompt_workspace_bytes(
-                    ctypes.byref(self.desc), seqs.batch, seqs.max_pages, Hq, n,
-                    starts is not None)
-                ws = torch.empty(nb // 4 + 4, dtype=torch.float32, device=self.device)
-                dkv_kv4_prompt_attn(self.c, seqs, Q, _dtype_code(Q.dtype), Hq, n,
-                                    *self._strides(Q), softmax_scale, window, out, lse, ws, nb,
-                                    handle)
-        return (out, lse) if return_lse else out
+        return self._attn("prompt", Q, Q, (seqs.batch, seqs.max_pages, Hq, n, int(starts is not None)),
+                          n, seqs, softmax_scale, window, out, return_lse)
 
     def device_status(self, stream=None) -> int:
         """Read and clear the pool's status word (synchronises)."""
-        ctx, _ = self._on(stream)
-        with ctx:
-            word = int(self.status.item())
-            if word:
-                self.status.zero_()
+        ctx = self._elsewhere(stream)
+        if ctx is not None:
+            with ctx:
+                return self.device_status()
+        word = int(self.status.item())
+        if word:
+            self.status.zero_()
         return word
