@@ -135,7 +135,7 @@ __device__ inline int find_seq(const View &v, int i) {
 // The block rule.  lo <= 0 <= hi: the block's extremes with 0 among them.
 // ---------------------------------------------------------------------------
 struct Block {
-    float s, r;        // scale and its reciprocal (1 for an all-zero block)
+    float s, r;        // scale and about its reciprocal (1 for an all-zero block)
     int zero;
     uint16_t meta;
 };
@@ -146,26 +146,38 @@ __device__ inline float clamp_in(float x) {
     return fminf(fmaxf(x, -32768.f), 32768.f);
 }
 
+// RN(x / s) for s of at most 7 significant bits and r within 1 ulp of 1 / s, as
+// far as rint() of it can tell.  q0 = RN(x r) is within 2.5 ulp, so x - s q0 has
+// few bits and the first FMA is exact; the second is RN of x / s + d, |d| <=
+// 2.5 * 2^-23 ulp.  x / s is never the midpoint of two floats (25 bits times an
+// odd factor of s is no 24-bit x) and lies at least 2^-8 ulp away from one, so d
+// cannot matter.  Quotients whose steps underflow are far below 1/2.
+__device__ inline float div7(float x, float s, float r) {
+    const float q = __fmul_rn(x, r);
+    return __fmaf_rn(__fmaf_rn(-s, q, x), r, q);
+}
+
 __device__ inline Block block_rule(float lo, float hi) {
     const float r = __fmul_rn(__fsub_rn(hi, lo), 1.0f / 15.0f);
-    float s;
-    if (r < 6.103515625e-05f)       // 2^-14: fp16's subnormals, steps of 2^-20
-        s = ceilf(r * 1048576.0f) * 9.5367431640625e-07f;
-    else                            // up to 7 significant bits
-        s = __uint_as_float((__float_as_uint(r) + 0x1FFFFu) & ~0x1FFFFu);
+    // up to 7 significant bits; below 2^-14 (fp16's subnormals) to a multiple of 2^-20
+    float s = __uint_as_float((__float_as_uint(r) + 0x1FFFFu) & ~0x1FFFFu);
+    if (r < 6.103515625e-05f) s = ceilf(r * 1048576.0f) * 9.5367431640625e-07f;
     Block b;
-    b.s = s > 0.f ? s : 1.f;
-    b.r = __frcp_rn(b.s);
-    b.zero = s > 0.f ? min(15, __float2int_rn(div_rn_markstein(-lo, b.s, b.r))) : 0;
-    b.meta = s > 0.f ? (uint16_t)(__half_as_ushort(__float2half_rn(s)) | b.zero) : (uint16_t)0;
+    const bool none = !(s > 0.f);
+    b.s = none ? 1.f : s;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(b.r) : "f"(b.s));
+    // rint by adding 1.5 * 2^23; at most 15, as s >= r
+    const float z = __fadd_rn(div7(-lo, b.s, b.r), 12582912.f);
+    b.zero = min(15, (int)(__float_as_uint(z) - 0x4B400000u));
+    b.meta = (uint16_t)(__half_as_ushort(__float2half_rn(s)) | b.zero);
     return b;
 }
 // An all-zero block (meta 0) takes s = 1, zero = 0: its elements are 0 or so
 // small that their range underflows, and their codes come out 0.
-__device__ inline int block_code(const Block &b, float x) {
-    return max(0, min(15, __float2int_rn(div_rn_markstein(x, b.s, b.r)) + b.zero));
-}
 
+// The V codes and meta of odd positions are stored mirrored, 15 - c with 15 - z
+// and -s: the same value, (c - z) s.  The tensor cores cut sums towards zero;
+// with every other sum of products turned around, the cuts do not add up.
 // Mirror of a V word / V meta halfword at position tok (its own inverse).
 __device__ inline uint32_t mirror_codes(uint32_t w, int tok) { return (tok & 1) ? ~w : w; }
 __device__ inline uint32_t mirror_meta(uint32_t m, int tok) { return (tok & 1) ? m ^ 0x800Fu : m; }
