@@ -558,21 +558,33 @@ split_kernel(View v, Split p) {
         const int n = (int)(u1 - u0);
         Cursor c = seek(v, p, u0), ci = c;
         uint32_t masks = 0;                 // 2 bits a stage: the records on their way
-        // issue: lane r fetches record r of the unit at ci into stage `slot`
-        auto issue = [&](int slot) {
-            const int pos = ci.first + ci.u * UT + lane * RT;
-            const uint8_t *src = nullptr;
-            if (lane < 2 && pos < ci.len) {
-                src = record(v, ci.b, ci.sq / p.nhg, pos, L::REC);
-                if (src && !range_ok(v.status, src, L::REC, v.pool, v.n_pages * v.page_bytes))
-                    src = nullptr;
+        // Lane r knows record r of the 16 units from ci's at `base` on (of one run):
+        // a unit's copies are issued by the two lanes that know its records.
+        const uint8_t *src = nullptr;
+        unsigned have = 0;
+        int base = 0, left = 0;             // units that the lanes still know
+        auto issue = [&](int slot) {        // the unit at ci into stage `slot`
+            if (left == 0) {
+                const int pos = ci.first + ci.u * UT + lane * RT;
+                src = nullptr;
+                if (pos < ci.len) {
+                    src = record(v, ci.b, ci.sq / p.nhg, pos, L::REC);
+                    if (src && !range_ok(v.status, src, L::REC, v.pool, v.n_pages * v.page_bytes))
+                        src = nullptr;
+                }
+                have = __ballot_sync(0xffffffffu, src != nullptr);
+                base = ci.u;
+                left = min(16, ci.nu - ci.u);
             }
-            const unsigned have = __ballot_sync(0xffffffffu, src != nullptr);
-            if (lane == 0) mbar_arrive_expect_tx(bar + slot, __popc(have) * L::REC);
-            __syncwarp();
-            if (src)
-                bulk_g2s(ring + slot * stage_bytes<L>() + lane * L::REC, src, L::REC, bar + slot);
-            masks = (masks & ~(3u << (2 * slot))) | have << (2 * slot);
+            const int k = ci.u - base;
+            const unsigned two = have >> (2 * k) & 3u;
+            // (a copy may be counted before its bytes are announced: the phase ends
+            // with the announcement at the earliest)
+            if (lane == 0) mbar_arrive_expect_tx(bar + slot, __popc(two) * L::REC);
+            if ((lane >> 1) == k && src)
+                bulk_g2s(ring + slot * stage_bytes<L>() + (lane & 1) * L::REC, src, L::REC, bar + slot);
+            masks = (masks & ~(3u << (2 * slot))) | two << (2 * slot);
+            --left;
             step(v, p, ci);
         };
         int issued = 0;
