@@ -80,11 +80,34 @@ __device__ inline int64_t warp_of(int64_t u, int64_t total, int64_t nw) {
     return u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q;
 }
 
-// Units of batch entries before b (all entries for b = B), a whole warp asking.
-__device__ inline int64_t units_before(const View &v, const Split &p, int b_end) {
+// Units of all batch entries, of those before b, and of one run of b; a whole
+// warp asking.
+__device__ inline void units_around(const View &v, const Split &p, int b, int64_t *total,
+                                    int64_t *before, int *own) {
+    const int lane = threadIdx.x & 31;
+    int64_t n = 0, m = 0;
+    int mine = 0;
+    for (int i = lane; i < v.B; i += 32) {
+        int first;
+        const int k = span(max(0, seq_len(v, i)), p.nq, p.q.window, &first);
+        n += k;
+        if (i < b) m += k;
+        if (i == b) mine = k;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        n += __shfl_xor_sync(0xffffffffu, n, o);
+        m += __shfl_xor_sync(0xffffffffu, m, o);
+    }
+    *total = n * p.nseq;
+    *before = m * p.nseq;
+    *own = __reduce_max_sync(0xffffffffu, mine);
+}
+// Units of all batch entries.
+__device__ inline int64_t units_of_all(const View &v, const Split &p) {
     const int lane = threadIdx.x & 31;
     int64_t n = 0;
-    for (int b = lane; b < b_end; b += 32) {
+    for (int b = lane; b < v.B; b += 32) {
         int first;
         n += span(max(0, seq_len(v, b)), p.nq, p.q.window, &first);
     }
@@ -549,7 +572,7 @@ split_kernel(View v, Split p) {
     pdl_trigger();
 
     const int w = blockIdx.x * WARPS + wi;
-    const int64_t total = units_before(v, p, v.B);
+    const int64_t total = units_of_all(v, p);
     const int64_t nw = warps_used(total, p.NW);
     int open = -1;
     Acc<L> acc;
@@ -678,34 +701,51 @@ merge_kernel(View v, Split p) {
     pdl_trigger();
     const int run = blockIdx.x, b = run / p.nseq, sq = run - b * p.nseq;
     const int h = threadIdx.x / (D / 4), c = threadIdx.x % (D / 4);
-    const int64_t total = units_before(v, p, v.B), nw = warps_used(total, p.NW);
-    int first;
-    const int nu = span(max(0, seq_len(v, b)), p.nq, p.q.window, &first);
-    const int64_t u0 = units_before(v, p, b) + (int64_t)sq * nu, u1 = u0 + nu;
+    int64_t total, u0;
+    int nu;
+    units_around(v, p, b, &total, &u0, &nu);
+    const int64_t nw = warps_used(total, p.NW);
+    u0 += (int64_t)sq * nu;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (nu > 0) {
+        const int64_t u1 = u0 + nu;
         const int64_t wa = warp_of(u0, total, nw), wb = warp_of(u1 - 1, total, nw);
-        // the warp that goes on to the next run left a record of its own
+        // the warp that goes on to the next run left a record of its own; the others
+        // of a CTA are in the record of its first one
         const bool closed = unit_of(wb + 1, total, nw) > u1;
         const int64_t last_open = closed ? wb - 1 : wb;
-        int64_t w = wa;
-        while (w <= wb) {
-            const float *r = p.ws + (w + run) * RF;
-            if (range_ok(v.status, r, RF * 4, p.ws, p.ws_floats * 4)) {
-                const float mr = r[h], lr = r[8 + h];
-                const float4 y = reinterpret_cast<const float4 *>(r + 16 + h * D)[c];
-                const float mx = fmaxf(m, mr), ref = mx == -INFINITY ? 0.f : mx;
-                const float f0 = ex2(m - ref), f1 = ex2(mr - ref);
-                l = fmaf(l, f0, lr * f1);
-                o.x = fmaf(o.x, f0, y.x * f1);
-                o.y = fmaf(o.y, f0, y.y * f1);
-                o.z = fmaf(o.z, f0, y.z * f1);
-                o.w = fmaf(o.w, f0, y.w * f1);
+        const int open = last_open >= wa ? (int)(last_open / WARPS - wa / WARPS) + 1 : 0;
+        const int n = open + (closed ? 1 : 0);
+        constexpr int AT_ONCE = 8;         // loads on their way
+        for (int k0 = 0; k0 < n; k0 += AT_ONCE) {
+            float mr[AT_ONCE], lr[AT_ONCE];
+            float4 y[AT_ONCE];
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const int k = k0 + i;
+                const int64_t w = k >= open ? wb : k == 0 ? wa : (wa / WARPS + k) * WARPS;
+                const float *r = p.ws + (w + run) * RF;
+                mr[i] = -INFINITY;
+                lr[i] = 0.f;
+                y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k < n && range_ok(v.status, r, RF * 4, p.ws, p.ws_floats * 4)) {
+                    mr[i] = r[h];
+                    lr[i] = r[8 + h];
+                    y[i] = reinterpret_cast<const float4 *>(r + 16 + h * D)[c];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const float mx = fmaxf(m, mr[i]), ref = mx == -INFINITY ? 0.f : mx;
+                const float f0 = ex2(m - ref), f1 = ex2(mr[i] - ref);
+                l = fmaf(l, f0, lr[i] * f1);
+                o.x = fmaf(o.x, f0, y[i].x * f1);
+                o.y = fmaf(o.y, f0, y[i].y * f1);
+                o.z = fmaf(o.z, f0, y[i].z * f1);
+                o.w = fmaf(o.w, f0, y[i].w * f1);
                 m = mx;
             }
-            // the other open warps of a CTA are in its first one's record
-            w = w <= last_open ? min((w / WARPS + 1) * WARPS, last_open + 1) : w + 1;
         }
     }
     const int kvh = sq / p.nhg, hv = (sq - kvh * p.nhg) * 8 + h;
