@@ -670,8 +670,8 @@ class Kv4Cache:
                 name = "block_table" if dims == 2 else "seq_lens" if x is seq_lens else "starts"
                 self._tensor(x, name, dims)
                 raise ValueError(f"{name} must be contiguous int32")
-        B, (rows, width) = len(seq_lens), block_table.shape
-        if rows != B or (starts is not None and len(starts) != B + 1):
+        (B,), (rows, width) = seq_lens.shape, block_table.shape
+        if rows != B or (starts is not None and starts.shape[0] != B + 1):
             raise ValueError("block_table, seq_lens and starts disagree about the batch")
         return dkv_kv4_batch(B, width, block_table.data_ptr(), seq_lens.data_ptr(),
                              None if starts is None else starts.data_ptr())
@@ -736,8 +736,8 @@ class Kv4Cache:
         seqs = self._batch(block_table, seq_lens, starts)
         if out is None:
             dtype = torch.float16 if dtype is None else dtype
-            out = (torch.empty(shape, dtype=dtype, device=self.device),
-                   torch.empty(shape, dtype=dtype, device=self.device))
+            k = self.status.new_empty(shape, dtype=dtype)
+            out = (k, torch.empty_like(k))
         else:
             for x in out:
                 self._tensor(x, "out")
@@ -757,20 +757,20 @@ class Kv4Cache:
         sizes: what its workspace depends on."""
         torch = self._torch
         shape, row, head, code = self._rows(rows, "Q")
+        # (like tensors that are at hand: half of torch.empty's time on the host)
         if out is None:
-            out = torch.empty(Q.shape, dtype=Q.dtype, device=self.device)
+            out = torch.empty_like(Q, memory_format=torch.contiguous_format)
         else:
             if out.shape != Q.shape or out.dtype != Q.dtype or not out.is_contiguous():
                 raise ValueError("out must be contiguous, of Q's shape and dtype")
             self._tensor(out, "out")
-        lse = torch.empty(Q.shape[:-1], dtype=torch.float32, device=self.device) \
-            if return_lse else None
+        lse = Q.new_empty(Q.shape[:-1], dtype=torch.float32) if return_lse else None
         if shape[0]:
             lib = self._lib
             size, call = (lib.dkv_kv4_decode_workspace_bytes, lib.dkv_kv4_decode_attn) \
                 if what == "decode" else (lib.dkv_kv4_prompt_workspace_bytes, lib.dkv_kv4_prompt_attn)
             nb = size(self._desc, *sizes)
-            ws = torch.empty(nb + 16, dtype=torch.uint8, device=self.device)
+            ws = self.status.new_empty(nb // 4 + 4)
             _check(call(self._pool, ctypes.byref(seqs), rows.data_ptr(), code, shape[1], n_queries,
                      row, head, softmax_scale, window, out.data_ptr(),
                      None if lse is None else lse.data_ptr(), ws.data_ptr(), nb,

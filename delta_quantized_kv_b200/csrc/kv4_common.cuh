@@ -23,6 +23,9 @@
 // exact in fp16; so is zero * scale.
 #pragma once
 
+#include <cuda_runtime.h>
+
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/dkv.h"
@@ -186,6 +189,20 @@ __device__ inline __half2 meta_scale(uint32_t m) { return u32_as_h2(m & 0xFFF0FF
 // zero points of two blocks as exact fp16 integers
 __device__ inline __half2 meta_zero(uint32_t m) {
     return __hsub2(u32_as_h2((m & 0x000F000Fu) | 0x64006400u), u32_as_h2(0x64006400u));
+}
+
+// Lets KERNEL have `bytes` of dynamic shared memory on the current device; the
+// attribute belongs to the device's copy of the kernel and is set once for each.
+template <typename Kernel>
+inline cudaError_t allow_smem_once(Kernel *kernel, int bytes, std::atomic<uint64_t> *done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (done->load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 }  // namespace kv4

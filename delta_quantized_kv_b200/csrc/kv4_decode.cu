@@ -805,10 +805,8 @@ cudaError_t split_ctas(const View &v, int Hq, int nq, int *ctas) {
 
 template <typename L, int DT>
 cudaError_t launch(const View &v, const Split &p, int ctas, cudaStream_t st) {
-    // (per device: the attribute belongs to the device's copy of the kernel)
-    cudaError_t e = cudaFuncSetAttribute(split_kernel<L, DT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_bytes<L>());
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem_once(split_kernel<L, DT>, smem_bytes<L>(), &done);
     if (e == cudaSuccess)
         e = launch_pdl(split_kernel<L, DT>, dim3(ctas), dim3(WARPS * 32), smem_bytes<L>(), st, v, p);
     if (e == cudaSuccess)

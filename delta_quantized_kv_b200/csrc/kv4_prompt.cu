@@ -1126,9 +1126,8 @@ int64_t floats_of(const Grid &g, int D) {
 
 template <typename L, int DT>
 cudaError_t launch(const View &v, const Prompt &p, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(prompt_kernel<L, DT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Smem<L::D>::BYTES);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem_once(prompt_kernel<L, DT>, Smem<L::D>::BYTES, &done);
     if (e == cudaSuccess)
         e = launch_pdl(prompt_kernel<L, DT>, dim3(p.ctas), dim3(THREADS), Smem<L::D>::BYTES, st, v,
                        p);
