@@ -257,7 +257,7 @@ __device__ inline int q_exponent(float mx) {
 // counts n + COST units, and the units of the batch are cut into equal runs, one
 // per CTA: a run may begin and end inside a job.
 // ---------------------------------------------------------------------------
-constexpr int COST = 2;            // of a job besides its tiles: queries in, results out
+constexpr int COST = 3;            // of a job besides its tiles (3: 653 us a prompt of 8192; 1, 2, 5: 750, 693, 652)
 constexpr int MIN_UNITS = 6;       // per CTA, where there are enough
 
 struct Seq {
