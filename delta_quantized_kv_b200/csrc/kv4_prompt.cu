@@ -253,12 +253,14 @@ __device__ inline int q_exponent(float mx) {
 
 // ---------------------------------------------------------------------------
 // Distribution of the work.  A job is 256 rows of one kv head of one sequence;
-// jobs stand in order of sequence, kv head and row.  A job of n position tiles
-// counts n + COST units, and the units of the batch are cut into equal runs, one
-// per CTA: a run may begin and end inside a job.
+// jobs stand in order of sequence, kv head and row.  A job counts the positions
+// it sees, times G, and COST position tiles more, as units: they grow by 256
+// from block to block until a window fills, so their sums are closed formulas.
+// The units of the batch are cut into equal runs, one per CTA: a run may begin
+// and end inside a job, and has its position tiles from and up to there.
 // ---------------------------------------------------------------------------
-constexpr int COST = 3;            // of a job besides its tiles (3: 653 us a prompt of 8192; 1, 2, 5: 750, 693, 652)
-constexpr int MIN_UNITS = 6;       // per CTA, where there are enough
+constexpr int COST = 3;            // (3: 653 us a prompt of 8192; 1, 2, 5: 750, 693, 652)
+constexpr int MIN_TILES = 6;       // of a run, where there are enough
 
 struct Seq {
     int n, len, s0, blocks;        // rows' tokens, length, first row, blocks of 256 rows
@@ -286,32 +288,28 @@ __device__ inline int tiles_of(const Prompt &p, const Seq &s, int blk, int *kv0)
     *kv0 = lo;
     return (last + 1 - lo + TN - 1) / TN;
 }
-// Units of one kv head of sequences b0 .. b0 + 31, lane by lane; a whole warp asks.
-__device__ inline int64_t seq_units(const View &v, const Prompt &p, int b0) {
-    const int lane = threadIdx.x & 31;
-    const Seq s = load_seq(v, p, b0 + lane);
-    int64_t mine = 0;
-    int kv;
-    if (__reduce_max_sync(0xffffffffu, s.blocks) <= 8) {
-        for (int i = 0; i < s.blocks; ++i) mine += tiles_of(p, s, i, &kv) + COST;
-        return mine;
-    }
-    for (int l = 0; l < 32; ++l) {
-        Seq t;
-        t.n = __shfl_sync(0xffffffffu, s.n, l);
-        t.len = __shfl_sync(0xffffffffu, s.len, l);
-        t.blocks = __shfl_sync(0xffffffffu, s.blocks, l);
-        int64_t x = 0;
-        for (int i = lane; i < t.blocks; i += 32) x += tiles_of(p, t, i, &kv) + COST;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == l) mine = x;
-    }
-    return mine;
+// Units of blocks 0 .. m - 1, and of block m.
+struct Units {
+    int64_t base, full;            // block i: base + 256 (i + 1), at most full
+    int64_t cost;
+};
+__device__ inline Units units_of(const Prompt &p, const Seq &s) {
+    Units u;
+    u.base = (int64_t)p.G * (s.len - s.n);
+    u.full = p.q.window > 0 ? (int64_t)p.G * p.q.window + 2 * TM : INT64_MAX;
+    u.cost = (int64_t)COST * TN * p.G;
+    return u;
 }
-__device__ inline int64_t ctas_used(int64_t total, int ctas) {
-    const int64_t n = (total + MIN_UNITS - 1) / MIN_UNITS;
-    return n < ctas ? n : ctas;
+__device__ inline int64_t units_before(const Units &u, int64_t m) {
+    const int64_t k = u.full <= u.base ? 0 : min(m, (u.full - u.base) / (2 * TM));
+    return u.base * k + TM * k * (k + 1) + (m > k ? (m - k) * u.full : 0) + m * u.cost;
+}
+__device__ inline int64_t units_at(const Units &u, int64_t m) {
+    return min(u.full, u.base + 2 * TM * (m + 1)) + u.cost;
+}
+__device__ inline int64_t ctas_used(int64_t total, int G, int ctas) {
+    const int64_t least = (int64_t)MIN_TILES * TN * G, n = total / least;
+    return n < 1 ? (total > 0) : n < ctas ? n : ctas;
 }
 // first unit of CTA c, and the CTA of unit u
 __device__ inline int64_t unit_of(int64_t c, int64_t total, int64_t n) {
@@ -332,20 +330,21 @@ struct Run {
 __device__ inline Run find_run(const View &v, const Prompt &p, int cta) {
     const int lane = threadIdx.x & 31;
     Run r{};
-    for (int b0 = 0; b0 < v.B; b0 += 32) {
-        int64_t u = seq_units(v, p, b0);
+    auto of_head = [&](int b) {                     // units of one kv head
+        const Seq s = load_seq(v, p, b);
+        return s.blocks > 0 ? units_before(units_of(p, s), s.blocks) : 0;
+    };
+    for (int b = lane; b < v.B; b += 32) r.total += of_head(b);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-        r.total += u;
-    }
+    for (int o = 16; o; o >>= 1) r.total += __shfl_xor_sync(0xffffffffu, r.total, o);
     r.total *= v.H;
-    r.n = ctas_used(r.total, p.ctas);
+    r.n = ctas_used(r.total, p.G, p.ctas);
     if (cta >= r.n) return r;                       // left = 0
     r.begin = unit_of(cta, r.total, r.n);
     r.left = unit_of(cta + 1, r.total, r.n) - r.begin;
     int64_t at = r.begin;
     for (int b0 = 0; b0 < v.B; b0 += 32) {
-        const int64_t u = seq_units(v, p, b0);
+        const int64_t u = b0 + lane < v.B ? of_head(b0 + lane) : 0;
         int64_t inc = u * v.H;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -355,30 +354,22 @@ __device__ inline Run find_run(const View &v, const Prompt &p, int cta) {
         const unsigned hit = __ballot_sync(0xffffffffu, inc > at);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            const int64_t one = __shfl_sync(0xffffffffu, u, l);      // of one head
+            const int64_t one = __shfl_sync(0xffffffffu, u, l);
             at -= __shfl_sync(0xffffffffu, inc, l) - one * v.H;
             r.b = b0 + l;
             r.kvh = (int)(at / one);
             at -= r.kvh * one;
             const Seq s = load_seq(v, p, r.b);
-            for (int i0 = 0; i0 < s.blocks; i0 += 32) {
-                int kv;
-                int n = i0 + lane < s.blocks ? tiles_of(p, s, i0 + lane, &kv) + COST : 0;
-                int64_t sum = n;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
-                    if (lane >= o) sum += y;
-                }
-                const unsigned in = __ballot_sync(0xffffffffu, sum > at);
-                if (in) {
-                    const int k = __ffs(in) - 1;
-                    r.blk = i0 + k;
-                    r.off = at - (__shfl_sync(0xffffffffu, sum, k) - __shfl_sync(0xffffffffu, n, k));
-                    return r;
-                }
-                at -= __shfl_sync(0xffffffffu, sum, 31);
+            const Units q = units_of(p, s);
+            int lo = 0, hi = s.blocks;              // the last block that begins at or before `at`
+            while (hi - lo > 1) {
+                const int mid = lo + (hi - lo) / 2;
+                if (units_before(q, mid) <= at) lo = mid;
+                else hi = mid;
             }
+            r.blk = lo;
+            r.off = at - units_before(q, lo);
+            return r;
         }
         at -= __shfl_sync(0xffffffffu, inc, 31);
     }
@@ -418,9 +409,17 @@ __device__ inline bool walk_next(const View &v, const Prompt &p, Walk *w, Job *j
     __syncwarp();
     while (!got && r.left > 0) {
         int kv0;
-        const int tiles = tiles_of(p, s, r.blk, &kv0), units = tiles + COST;
+        const int tiles = tiles_of(p, s, r.blk, &kv0);
+        const Units u = units_of(p, s);
+        const int64_t units = units_at(u, r.blk);
         const int64_t rest = units - r.off, take = rest < r.left ? rest : r.left;
-        const int t0 = max(0, (int)r.off - COST), t1 = max(0, (int)(r.off + take) - COST);
+        // tiles up to a unit of the job; behind the cost, `each` units a tile (at most
+        // 128 G + 257, less than the least run, so that every run inside a job has one)
+        const int64_t each = (units - u.cost + tiles - 1) / tiles;
+        auto upto = [&](int64_t x) {
+            return x <= u.cost ? 0 : x >= units ? tiles : (int)min((int64_t)tiles, (x - u.cost) / each);
+        };
+        const int t0 = upto(r.off), t1 = upto(r.off + take);
         j->b = r.b;
         j->kvh = r.kvh;
         j->row0 = r.blk * 2 * TM;
@@ -1102,7 +1101,7 @@ cudaError_t sm_count(int *n) {
     return cudaSuccess;
 }
 
-// The grid: one CTA per SM, fewer where the call cannot have MIN_UNITS for each;
+// The grid: one CTA per SM, fewer where the call cannot have MIN_TILES for each;
 // rows of a partial result.
 struct Grid {
     int ctas, slot;
@@ -1115,7 +1114,7 @@ cudaError_t grid_of(const View &v, int Hq, Grid *g) {
     // every sequence may end inside a block
     const int64_t jobs = (rows / (2 * TM) + (v.B < v.n_rows ? v.B : v.n_rows)) * v.H;
     const int64_t tiles = (int64_t)v.max_pages * v.page_size / TN + 2;
-    const int64_t ctas = (jobs * (tiles + COST) + MIN_UNITS - 1) / MIN_UNITS;
+    const int64_t ctas = (jobs * (tiles + COST) + MIN_TILES - 1) / MIN_TILES;
     g->ctas = (int)(ctas < sms ? ctas : sms);
     g->slot = (int)(rows < 2 * TM ? rows : 2 * TM);
     return cudaSuccess;
