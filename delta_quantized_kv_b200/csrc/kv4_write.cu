@@ -200,6 +200,8 @@ append_kernel(View v, const void *K, const void *V, int64_t k_tok, int64_t k_hea
     const int hb = blockIdx.z * heads, he = min(v.H, hb + heads);      // this warp's heads
     int b = find_seq(v, first);
     for (int token = first; token < last; ++token) {
+        if (v.starts)
+            while (b < v.B && v.starts[b + 1] <= token) ++b;
         if (b >= v.B) break;               // padding
         Raw<DT> a[AHEAD];
         auto load = [&](int h0) {
