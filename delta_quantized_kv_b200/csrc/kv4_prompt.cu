@@ -668,12 +668,11 @@ prompt_kernel(View v, Prompt p) {
                                   (p.q.window > 0 && kv <= pmax - p.q.window) || vm != 0x0303u;
                 uint32_t w[SN / 2];
                 uint64_t la, lb;
-                // The weights are taken with the reference as it stands, and the
-                // scores' maximum alongside; where it has risen too far (seldom
-                // behind a job's first step) the step is done again.
-                bool find = j == 0;            // only look for the maximum
+                // A job's first step takes its reference from the maximum.  Behind it the
+                // weights are taken with the reference as it stands, and the scores'
+                // maximum alongside; where it has risen too far (seldom) the step is
+                // done again.
                 while (true) {
-                    const uint64_t c2 = f2(c1, c1), r2 = f2(neg, neg);
                     uint32_t s0[32], s1[32];
                     tm_ld32(s0, tS);
                     tm_ld32(s1, tS + 32);
@@ -691,34 +690,32 @@ prompt_kernel(View v, Prompt p) {
                         hide(s1, see(1));
                     }
                     const float mx = fmaxf(max32(s0), max32(s1)) * c1;
-                    la = lb = 0;
-                    if (!find) {
-                        weights(s0, c2, r2, w, la, lb);
-                        weights(s1, c2, r2, w + 16, la, lb);
+                    if (j == 0 && mx > -INFINITY) {
+                        neg = 7.f - mx;
+                        top = mx + 8.f;
                     }
+                    const uint64_t c2 = f2(c1, c1), r2 = f2(neg, neg);
+                    la = lb = 0;
+                    weights(s0, c2, r2, w, la, lb);
+                    weights(s1, c2, r2, w + 16, la, lb);
                     // (NaN scores leave mx to the others; their weights are NaN)
                     const bool up = mx > top;
-                    const bool move = __any_sync(0xffffffffu, up);
-                    if (!move && !find) break;
-                    find = false;
-                    if (!move) continue;
+                    if (!__any_sync(0xffffffffu, up)) break;
                     const float f = top == -INFINITY ? 0.f : ex2(7.f - neg - mx);
-                    if (j > 0) {
-                        // O must be at rest
-                        ok = warp_wait(bars + OFULL + 2 * qi + (h ^ 1), (at - 1) >> 1 & 1);
-                        if (!ok) break;
-                        tm_fence_after();
+                    // O must be at rest
+                    ok = warp_wait(bars + OFULL + 2 * qi + (h ^ 1), (at - 1) >> 1 & 1);
+                    if (!ok) break;
+                    tm_fence_after();
 #pragma unroll
-                        for (int i = 0; i < L::D / 16; ++i) {
-                            uint32_t o[16];
-                            tm_ld16(o, tO + 16 * i);
-                            tm_wait_ld16(o);
+                    for (int i = 0; i < L::D / 16; ++i) {
+                        uint32_t o[16];
+                        tm_ld16(o, tO + 16 * i);
+                        tm_wait_ld16(o);
 #pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                o[k] = __float_as_uint(up ? __uint_as_float(o[k]) * f
-                                                          : __uint_as_float(o[k]));
-                            tm_st16(tO + 16 * i, o);
-                        }
+                        for (int k = 0; k < 16; ++k)
+                            o[k] = __float_as_uint(up ? __uint_as_float(o[k]) * f
+                                                      : __uint_as_float(o[k]));
+                        tm_st16(tO + 16 * i, o);
                     }
                     if (up) {
                         l2 = fma2(l2, f2(f, f), 0);
