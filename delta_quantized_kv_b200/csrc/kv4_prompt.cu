@@ -185,8 +185,8 @@ __device__ inline void tm_st16(uint32_t addr, const uint32_t *r) {
 __device__ inline bool warp_wait(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
 }
-// Registers of this warpgroup.  640 threads are launched with 96 each; 2 x 152
-// + 2 x 64 + 48 = 5 x 96.
+// Registers of this warpgroup.  640 threads are launched with 96 each; 2 x 144
+// + 2 x 72 + 48 = 5 x 96.
 template <int N>
 __device__ inline void regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
@@ -582,7 +582,7 @@ prompt_kernel(View v, Prompt p) {
 
     if (wg < 2) {
         // ---------------- softmax ------------------------------------------
-        regs_up<152>();
+        regs_up<144>();
         const int qi = wg;
         const uint32_t lane_base = (uint32_t)(warp & 3) << 21;
         const uint32_t tSP = tm + lane_base + qi * 128, tO = tm + lane_base + 256 + qi * L::D;
@@ -798,7 +798,7 @@ prompt_kernel(View v, Prompt p) {
         if (!ok) set_status(v.status, DKV_DEV_TIMEOUT);
     } else if (wg < 4) {
         // ---------------- dequantisation: K (2), V (3) ---------------------
-        regs_down<64>();
+        regs_down<72>();
         const bool isk = wg == 2;
         uint64_t *full = bars + (isk ? KFULL : VFULL), *free_ = bars + (isk ? KFREE : VFREE);
         constexpr int NM = (L::NB + 1) / 2;         // meta words: two blocks each
@@ -881,7 +881,7 @@ prompt_kernel(View v, Prompt p) {
             const uint8_t *rec = more ? locate(&here) : nullptr;      // the tile after
             if (j >= STAGES && !warp_wait(free_ + st, ph ^ 1)) { ok = false; break; }
             uint8_t *dst = smem + (isk ? S::K : S::V) + st * S::TILE + tid * 128;
-            // four words at a time; the next tile's take their place
+            // four words at a time
             if (isk) {
                 if (lane == 0)          // two records a warp: lanes 0..15 and 16..31
                     reinterpret_cast<volatile uint8_t *>(valid + (j & 3))[warp & 3] =
@@ -900,7 +900,6 @@ prompt_kernel(View v, Prompt p) {
                         const Meta &q = m[c8 * 8 / L::G];
                         y[k] = dequant8(w[k], q.s, q.z1024, q.z64);
                     }
-                    load(rec, i);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int c8 = 4 * (k % L::NJ) + (4 * i + k) / L::NJ;
@@ -926,7 +925,6 @@ prompt_kernel(View v, Prompt p) {
                         const Meta &q = m[L::D == 128 ? k & 1 : 0];
                         y[k] = dequant8(w[k], q.s, q.z1024, q.z64);
                     }
-                    load(rec, i);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         // D = 128: words 2 c + u of chunk c ^ flip
@@ -936,9 +934,12 @@ prompt_kernel(View v, Prompt p) {
                     }
                 }
             }
-            load_meta(rec);
             fence_proxy_async();
             warp_arrive(full + st);
+            // the next tile's words, behind the fence: it waits for loads too
+#pragma unroll
+            for (int i = 0; i < L::D / 32; ++i) load(rec, i);
+            load_meta(rec);
         }
         if (!ok) set_status(v.status, DKV_DEV_TIMEOUT);
     } else {
