@@ -107,8 +107,9 @@ dkv_status check_query(const View &v, const void *Q, int32_t q_dtype, int32_t Hq
     const dkv_status s = check_rows(Q, q_dtype, row, head);
     if (s != DKV_OK) return s;
     if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(ws, 16)) return DKV_EALIGN;
+    // a window past every position is none (and sums with it stay in 32 bits)
     *q = Query{Q, const_cast<void *>(out), const_cast<float *>(lse), row, head, q_dtype, Hq,
-               window, scale};
+               window > kMaxPositions ? 0 : window, scale};
     return DKV_OK;
 }
 

@@ -11,6 +11,11 @@
 // sequence leaves about one record per CTA that touches it.  The merge kernel
 // joins them.
 //
+// Measured on one B200: 16 sequences of 32768 positions, 64 heads over 8, D 128,
+// bf16: 163 us, 3.7 TB/s of packed cache.  Bound by instructions, not by DRAM:
+// 774 a unit, 60 % of the issue slots and of the ALU's (masks and shifts of the
+// codes), the tensor cores at 22 %.
+//
 // Mathematics.  x^ = (c - z) s, so with the sum over a block's channels
 //   q . k^ = sum_b s_b (q_b . c_b) + sum_b (s_b z_b) (-sum q_b):
 // the codes go into the MMA as they are -- a masked nibble IS the fp16
@@ -40,9 +45,9 @@ namespace {
 
 constexpr int WARPS = 8;          // per CTA
 constexpr int CTAS_PER_SM = 2;    // 16 warps: 128 registers each
-constexpr int NST = 3;            // units in flight per warp
+constexpr int NST = 3;            // units in flight per warp (2: the same times)
 constexpr int UT = 2 * RT;        // positions per unit
-constexpr int64_t MIN_UNITS = 2;  // per warp, where there are enough
+constexpr int64_t MIN_UNITS = 2;  // per warp (one user's 4096 positions: 13.8 us with 1 or 2, 16.4 with 4)
 
 struct Split {
     Query q;

