@@ -166,6 +166,7 @@ dkv_status check_decode(const dkv_cache *cache, const void *Q, int32_t q_dtype, 
 }  // namespace
 
 dkv_status dkv::validate_cache(const dkv_cache *c) { return check_cache(c); }
+int dkv::debug_fault() { return g_debug_fault; }
 
 extern "C" {
 

@@ -13,6 +13,9 @@ namespace dkv {
 // launch: DKV_OK, or the status those entry points return for it.
 dkv_status validate_cache(const dkv_cache *c);
 
+// What dkv_debug_set_fault last set (test support).
+int debug_fault();
+
 struct CacheView;
 
 cudaError_t launch_encode(const CacheView &cv, const void *K, const void *V, int dtype,

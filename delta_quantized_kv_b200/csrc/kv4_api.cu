@@ -4,6 +4,7 @@
 #include <cstring>
 
 #include "../../include/dkv.h"
+#include "dkv_internal.h"
 #include "kv4_common.cuh"
 #include "kv4_internal.h"
 
@@ -212,6 +213,7 @@ dkv_status dkv_kv4_decode_attn(const dkv_kv4_pool *pool, const dkv_kv4_batch *se
     if (ws_bytes < (size_t)need * sizeof(float)) return DKV_ECAPACITY;
     return cuda_status(dkv::kv4::launch_decode(v, pool->desc.head_dim, pool->desc.group, q,
                                                n_queries, static_cast<float *>(workspace), need,
+                                               dkv::debug_fault(),
                                                static_cast<cudaStream_t>(stream)));
 }
 

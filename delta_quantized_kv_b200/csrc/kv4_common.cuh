@@ -191,6 +191,12 @@ __device__ inline __half2 meta_zero(uint32_t m) {
     return __hsub2(u32_as_h2((m & 0x000F000Fu) | 0x64006400u), u32_as_h2(0x64006400u));
 }
 
+// A bounded wait whose outcome the whole warp shares: each lane has a clock of
+// its own to give up by, and what follows a wait takes all lanes.
+__device__ inline bool warp_wait(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+}
+
 // Lets KERNEL have `bytes` of dynamic shared memory on the current device; the
 // attribute belongs to the device's copy of the kernel and is set once for each.
 template <typename Kernel>

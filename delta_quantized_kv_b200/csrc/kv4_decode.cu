@@ -55,6 +55,7 @@ struct Split {
     float *ws;
     int64_t ws_floats;
     int NW;                 // warps of the grid
+    int unsent;             // bytes announced of each unit that no copy brings: 0 but in tests
 };
 
 template <int D>
@@ -580,6 +581,7 @@ split_kernel(View v, Split p) {
     const int64_t total = units_of_all(v, p);
     const int64_t nw = warps_used(total, p.NW);
     int open = -1;
+    bool dead = false;                      // a wait ran out
     Acc<L> acc;
     if (total > 0 && w < nw) {
         const int64_t u0 = unit_of(w, total, nw), u1 = unit_of(w + 1, total, nw);
@@ -608,7 +610,7 @@ split_kernel(View v, Split p) {
             const unsigned two = have >> (2 * k) & 3u;
             // (a copy may be counted before its bytes are announced: the phase ends
             // with the announcement at the earliest)
-            if (lane == 0) mbar_arrive_expect_tx(bar + slot, __popc(two) * L::REC);
+            if (lane == 0) mbar_arrive_expect_tx(bar + slot, __popc(two) * L::REC + p.unsent);
             if ((lane >> 1) == k && src)
                 bulk_g2s(ring + slot * stage_bytes<L>() + (lane & 1) * L::REC, src, L::REC, bar + slot);
             masks = (masks & ~(3u << (2 * slot))) | two << (2 * slot);
@@ -620,8 +622,8 @@ split_kernel(View v, Split p) {
         QFrag<L> q;
         acc_reset(acc);
         int cur = -1, slot = 0, parity = 0;
-        bool dead = false;
-        for (int i = 0; i < n; ++i) {
+        int i = 0;
+        for (; i < n; ++i) {
             const int run = c.b * p.nseq + c.sq;
             if (run != cur) {
                 if (cur >= 0) {             // the last run ended inside this warp's units
@@ -632,22 +634,17 @@ split_kernel(View v, Split p) {
                 cur = run;
                 load_q<L, DT>(v, p, c.b, c.sq, c.len, q);
             }
-            if (!mbar_wait_bounded(bar + slot, parity)) {
-                set_status(v.status, DKV_DEV_TIMEOUT);
-                dead = true;
-            }
+            dead = !warp_wait(bar + slot, parity);
+            if (dead) break;
             const int pos = c.first + c.u * UT;
             const bool edge = pos + UT > c.len - p.nq + 1 ||
                               (p.q.window > 0 && pos < c.len - p.q.window);
-            if (!dead)
-                unit<L, DT == DKV_F16>(ring + slot * stage_bytes<L>(), masks >> (2 * slot) & 3,
-                                       pos, edge, p.q.window, q, acc);
+            unit<L, DT == DKV_F16>(ring + slot * stage_bytes<L>(), masks >> (2 * slot) & 3, pos,
+                                   edge, p.q.window, q, acc);
             __syncwarp();
-            if (!dead && issued < n) {
+            if (issued < n) {
                 issue(slot);
                 ++issued;
-            } else if (dead && i + 1 >= issued) {
-                break;                      // every copy in flight has been waited for
             }
             step(v, p, c);
             if (++slot == NST) {
@@ -655,12 +652,24 @@ split_kernel(View v, Split p) {
                 parity ^= 1;
             }
         }
-        open = cur;
+        open = dead ? -1 : cur;
+        if (dead) {
+            if (lane == 0) set_status(v.status, DKV_DEV_TIMEOUT);
+            for (; i < issued; ++i) {       // the copies on their way, once more
+                warp_wait(bar + slot, parity);
+                if (++slot == NST) {
+                    slot = 0;
+                    parity ^= 1;
+                }
+            }
+        }
     }
     // Runs still open: warps of this CTA in the same run are joined by the
     // first of them.
     if (lane == 0) owner[wi] = open;
-    __syncthreads();                        // every ring is idle now
+    // Every ring is idle now, but for one whose copies did not come: they may still
+    // land where the records would stand, and the call's outputs are lost anyway.
+    if (__syncthreads_or(dead)) return;
     float *recs = reinterpret_cast<float *>(smem);
     if (open >= 0) put_record(recs + wi * RF, acc);
     __syncthreads();
@@ -837,7 +846,7 @@ cudaError_t decode_workspace_floats(const View &v, int D, int Hq, int nq, int64_
 }
 
 cudaError_t launch_decode(const View &v, int D, int G, const Query &q, int nq, float *ws,
-                          int64_t ws_floats, cudaStream_t st) {
+                          int64_t ws_floats, int fault, cudaStream_t st) {
     Split p;
     p.q = q;
     p.nq = nq;
@@ -850,6 +859,7 @@ cudaError_t launch_decode(const View &v, int D, int G, const Query &q, int nq, f
     const cudaError_t e = split_ctas(v, q.Hq, nq, &ctas);
     if (e != cudaSuccess) return e;
     p.NW = ctas * WARPS;
+    p.unsent = fault == 1 ? 16 : 0;
     if (D == 128)
         return G == 32 ? launch_dt<Lay<128, 32>>(v, p, ctas, st)
                        : launch_dt<Lay<128, 64>>(v, p, ctas, st);

@@ -28,10 +28,10 @@ struct Query {
     float scale;
 };
 
-// Decode: nq query rows a sequence (rows b * nq + t).
+// Decode: nq query rows a sequence (rows b * nq + t).  fault: as dkv_debug_set_fault sets it.
 cudaError_t decode_workspace_floats(const View &v, int D, int Hq, int nq, int64_t *floats);
 cudaError_t launch_decode(const View &v, int D, int G, const Query &q, int nq, float *ws,
-                          int64_t ws_floats, cudaStream_t st);
+                          int64_t ws_floats, int fault, cudaStream_t st);
 
 // Prompt: ragged query rows (v.starts, v.n_rows), or the same number each.
 cudaError_t prompt_workspace_floats(const View &v, int D, int Hq, int64_t *floats);

@@ -187,10 +187,6 @@ __device__ inline void tm_st16(uint32_t addr, const uint32_t *r) {
         : "memory");
 }
 
-// A bounded wait whose outcome the whole warp shares.
-__device__ inline bool warp_wait(uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
-}
 // Registers of this warpgroup.  640 threads are launched with 96 each; 2 x 144
 // + 2 x 72 + 48 = 5 x 96.
 template <int N>

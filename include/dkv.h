@@ -355,7 +355,8 @@ dkv_status dkv_lr_decode_attn(const dkv_lr_tensor *K, const dkv_lr_tensor *V, in
  *    not defined, but nothing outside the rows and the sequences' pages is
  *    touched).  DKV_DEV_BAD_PAGE: a block-table entry outside [0, n_pages)
  *    where a position is needed (its token is not stored or read, or not seen
- *    by the queries).
+ *    by the queries).  DKV_DEV_TIMEOUT: a pipeline wait ran out; the outputs of
+ *    that attention call are meaningless.
  *  - Sequences may share pages to read.  A page that a call writes must belong
  *    to one sequence in that call: two rows on one position leave either
  *    row's bytes.
@@ -493,12 +494,13 @@ dkv_status dkv_dequantize(const dkv_cache *cache, float *out, void *stream);
 dkv_status dkv_get_device_status(const dkv_cache *cache, int32_t *host_out, void *stream);
 
 /* Test support for failure detection (no counterpart on the pages).  With
- * mode 1, later decode-attention split launches from this process arm their
- * copy barriers without issuing the copies, so every bounded pipeline wait
- * runs out (after about a second) and the kernel records DKV_DEV_TIMEOUT in
- * the status word and returns, instead of hanging; the outputs of such a
- * launch are meaningless.  With mode 2, those launches are told the workspace
- * is two partial records smaller than it is: the bounds-checked build
+ * mode 1, later decode-attention split launches from this process (those of
+ * dkv_kv4_decode_attn among them) arm their copy barriers for bytes that no
+ * copy brings, so every bounded pipeline wait runs out (after about a second)
+ * and the kernel records DKV_DEV_TIMEOUT in the status word and returns,
+ * instead of hanging; the outputs of such a launch are meaningless.  With mode
+ * 2, those launches (but for dkv_kv4_decode_attn's) are told the workspace is
+ * two partial records smaller than it is: the bounds-checked build
  * (DKV_CHECKED) then records DKV_DEV_BOUNDS and skips the last record's
  * writes (the buffer itself is large enough, so nothing is touched out of
  * range); other builds ignore it.  Mode 0 restores normal operation.  Nothing
