@@ -25,12 +25,14 @@
 // block sums, is an fp16 hi + lo pair.  For the output,
 //   sum_p P_p v^_p = sum_p (P_p s_pb) c_p - sum_p P_p (s_pb z_pb):
 // the weights are rounded to fp16 once (P); the product P s is taken as fp16
-// hi for bf16 outputs, and as an exact hi + lo pair (two MMAs) for fp16 ones,
-// whose own rounding is 8 times finer.
+// hi for bf16 outputs, and as a hi + lo pair (two MMAs) for fp16 ones, whose own
+// rounding is 8 times finer: exact for P s from 2^-7 on.
 // Ranges: a query is scaled by a power of two so its largest element lies in
-// [2^14, 2^15); P is scaled by 2^k with k from the largest V scale met so far
-// (P s <= 2^14), as part of the running maximum, so rescaling is the online
-// softmax's own.
+// [2^14, 2^15); P is scaled by 2^k with k from the largest V scale that the
+// warp's queries have seen so far (P s <= 2^14, k <= 15), as part of the running
+// maximum, so rescaling is the online softmax's own.  Small products end in
+// fp16's subnormals: with the largest weight as 1, a weight times a scale is off
+// by at most 2^-25-k, which is 2^-38 of the largest scale seen, or 2^-40.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -322,10 +324,11 @@ __device__ inline void acc_reset(Acc<L> &a) {
     a.thr = 0x38003800u;   // 0.5
 }
 
-// One unit: `nrec` bit mask of the records that are there, pos of the first.
+// One unit: bit mask of the records that are there, pos of the first's positions;
+// edge: some query does not see all 32 of them, and [lo, hi) are those that any sees.
 template <typename L, bool LO>
-__device__ inline void unit(const uint8_t *st, int mask, int pos, bool edge, int window,
-                            const QFrag<L> &q, Acc<L> &a) {
+__device__ inline void unit(const uint8_t *st, int mask, int pos, bool edge, int lo, int hi,
+                            int window, const QFrag<L> &q, Acc<L> &a) {
     constexpr int NB = L::NB, NJ = L::NJ;
     constexpr uint32_t M0 = 0x000F000Fu, M1 = 0x00F000F0u;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -407,6 +410,14 @@ __device__ inline void unit(const uint8_t *st, int mask, int pos, bool edge, int
                 const bool seen = at < q.lim[i & 1] && (window <= 0 || at >= q.lim[i & 1] - window);
                 if (!seen) x[r][i] = -INFINITY;
             }
+            // nor do leftovers behind the length, or before every window, have a
+            // say in the weights' power of two
+            auto keep = [&](int at) {
+                return (at >= lo && at < hi ? 0xFFFFu : 0u) |
+                       (at + 4 >= lo && at + 4 < hi ? 0xFFFF0000u : 0u);
+            };
+            zm[r][0] &= keep(pos + r * RT + t);
+            zm[r][1] &= keep(pos + r * RT + t + 8);
         }
     }
     // the largest V scale bounds the weights' power of two
@@ -639,8 +650,9 @@ split_kernel(View v, Split p) {
             const int pos = c.first + c.u * UT;
             const bool edge = pos + UT > c.len - p.nq + 1 ||
                               (p.q.window > 0 && pos < c.len - p.q.window);
+            const int lo = p.q.window > 0 ? c.len - p.nq + 1 - p.q.window : 0;
             unit<L, DT == DKV_F16>(ring + slot * stage_bytes<L>(), masks >> (2 * slot) & 3, pos,
-                                   edge, p.q.window, q, acc);
+                                   edge, lo, c.len, p.q.window, q, acc);
             __syncwarp();
             if (issued < n) {
                 issue(slot);

@@ -419,10 +419,13 @@ dkv_status dkv_kv4_read(const dkv_kv4_pool *pool, const dkv_kv4_batch *seqs, voi
  * [batch * n_queries][n_q_heads], the natural log of the sum of exp(score).  A
  * query that sees nothing gives zeros and -inf.  seqs->starts is not read.
  * Query head h reads kv head h / (n_q_heads / n_kv_heads).  Scores, softmax
- * statistics and sums are fp32; the weights are rounded to fp16 once.  1 <=
- * n_queries <= 16.  DKV_F32 queries: DKV_EUNSUPPORTED.  Two launches.
- * workspace: device scratch, 16-byte aligned, of >= the _workspace_bytes (for
- * the current device), used by one call at a time. */
+ * statistics and sums are fp32; the weights are rounded to fp16 once, and for
+ * bf16 outputs once more with their V block's scale.  (These products, the
+ * largest weight being 1, also lose what lies below 2^-38 of the largest V
+ * scale that the sequence's queries see, or below 2^-40.)  1 <= n_queries <=
+ * 16.  DKV_F32 queries: DKV_EUNSUPPORTED.  Two launches.  workspace: device
+ * scratch, 16-byte aligned, of >= the _workspace_bytes (for the current
+ * device), used by one call at a time. */
 size_t dkv_kv4_decode_workspace_bytes(const dkv_kv4_desc *desc, int32_t batch, int32_t max_pages,
                                       int32_t n_q_heads, int32_t n_queries);
 dkv_status dkv_kv4_decode_attn(const dkv_kv4_pool *pool, const dkv_kv4_batch *seqs, const void *Q,
@@ -435,11 +438,11 @@ dkv_status dkv_kv4_decode_attn(const dkv_kv4_pool *pool, const dkv_kv4_batch *se
  * in the rows that seqs->starts gives each sequence (the chunk's own keys and
  * values already appended; a chunk may be of any length, one row too).  The
  * query of position p sees the positions max(0, p - window + 1) .. p (window
- * 0: all up to p).  Arguments, formula, types and precision as for
- * dkv_kv4_decode_attn, with out [n_rows][n_q_heads][D] and lse
- * [n_rows][n_q_heads].  A sequence whose starts pass n_rows is skipped too
- * (DKV_DEV_BAD_SEQLEN).  n_rows * n_q_heads <= 2^30.  Two launches.  ragged:
- * whether seqs->starts will be given. */
+ * 0: all up to p).  Arguments, formula and types as for dkv_kv4_decode_attn,
+ * with out [n_rows][n_q_heads][D] and lse [n_rows][n_q_heads]; the weights are
+ * rounded to fp16 once and multiplied with the values held.  A sequence whose
+ * starts pass n_rows is skipped too (DKV_DEV_BAD_SEQLEN).  n_rows * n_q_heads
+ * <= 2^30.  Two launches.  ragged: whether seqs->starts will be given. */
 size_t dkv_kv4_prompt_workspace_bytes(const dkv_kv4_desc *desc, int32_t batch, int32_t max_pages,
                                       int32_t n_q_heads, int32_t n_rows, int32_t ragged);
 dkv_status dkv_kv4_prompt_attn(const dkv_kv4_pool *pool, const dkv_kv4_batch *seqs, const void *Q,

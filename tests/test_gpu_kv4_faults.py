@@ -31,3 +31,46 @@ def test_a_wait_that_runs_out(dkv_gpu, D, group, dtype):
     assert status == dkv_gpu.DEV_TIMEOUT and took < 30
     assert torch.equal(cache.decode_attn(q, 0.1, table, end), good)
     assert cache.device_status() == 0
+
+
+def attention_of(ks, vs, q, group, pos, scale, window):
+    G = q.shape[1] // ks.shape[1]
+    return [R.attention(q[:, h].double().cpu().numpy(), R.held(ks[:, h // G], group), R.held(vs[:, h // G], group),
+                        R.step(ks[:, h // G], group), R.step(vs[:, h // G], group), pos, scale, window)
+            for h in range(q.shape[1])]
+
+
+@pytest.mark.parametrize("D,group", [(128, 32), (128, 64), (64, 32), (64, 64)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("nq,window", [(1, 0), (1, 13), (3, 0), (3, 37)])
+def test_values_that_no_query_sees_leave_every_bit(dkv_gpu, D, group, dtype, nq, window):
+    """Huge values behind the lengths (a recycled page's) and before the windows,
+    small ones where the queries look: the bits of a cache that holds zeros there."""
+    H, G, page, lens = 2, 3, 32, [20, 45, 71, 8, 64]
+    rng = np.random.default_rng(D + group + nq + window)
+    t = R.Tables(lens, page, 3)
+    table, end = t.dev()
+    full = [-(-n // page) * page for n in lens]
+    first = np.concatenate([[0], np.cumsum(full)])
+    k = rng.normal(size=(first[-1], H, D)).astype(np.float32)
+    v = (rng.normal(size=(first[-1], H, D)) * 1e-2).astype(np.float32)
+    seen = np.zeros(first[-1], bool)
+    for b, n in enumerate(lens):
+        lo = max(0, n - nq + 1 - window) if window else 0
+        seen[first[b] + lo:first[b] + n] = True
+    q = torch.from_numpy(rng.normal(size=(len(lens), nq, H * G, D)) * 3).to(dtype).cuda()
+    scale, got = 1 / D ** 0.5, []
+    for far in (0.0, 3e4):
+        x = np.where(seen[:, None, None], v, np.where(rng.random(v.shape) < 0.5, far, -far)).astype(np.float32)
+        cache = dkv_gpu.Kv4Cache(t.n_pages, H, head_dim=D, page_size=page, group=group)
+        cache.append(torch.from_numpy(k).to(dtype).cuda(), torch.from_numpy(x).to(dtype).cuda(), table,
+                     torch.tensor(full, dtype=torch.int32).cuda(), R.starts_of(full))
+        got.append(cache.decode_attn(q, scale, table, end, window=window, return_lse=True))
+        assert cache.device_status() == 0
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    kk, vv = (torch.from_numpy(y).to(dtype).float().numpy() for y in (k, v))
+    for b, n in enumerate(lens):
+        rows = slice(first[b], first[b] + n)
+        want = attention_of(kk[rows], vv[rows], q[b], group, n - nq + np.arange(nq), scale, window)
+        R.check(got[1][0][b], got[1][1][b], want, dtype)
