@@ -12,6 +12,7 @@ its ``dkv_cache`` descriptor.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from pathlib import Path
 
@@ -622,10 +623,12 @@ class Kv4Cache:
     (device int32 [batch], the call's own tokens included) and, for ragged
     calls, the first row of each sequence (`starts`, device int32 [batch + 1];
     None: the same number of rows for each).  Row i of a sequence's n rows
-    stands for position seq_len - n + i.  Every call launches on `stream`
-    (default: the current stream of the cache's device) and takes its scratch
-    and outputs from torch's allocator on that stream, so calls may be captured
-    into graphs and run on several streams at once.
+    stands for position seq_len - n + i.  Every call, the constructor too,
+    launches on `stream` (default: the current stream of the cache's device)
+    and takes its memory from torch's allocator on that stream, so calls may be
+    captured into graphs and run on several streams at once.  As everywhere in
+    torch, streams that share tensors (the pages among them) are put in order by
+    the caller.
     """
 
     def __init__(self, n_pages, n_kv_heads, head_dim=128, page_size=64, group=32, device="cuda",
@@ -640,13 +643,15 @@ class Kv4Cache:
             raise ValueError("a Kv4Cache lives on a CUDA device")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
-        self.pool = torch.empty(n_pages * pb + 256, dtype=torch.uint8, device=self.device)
-        self.status = torch.empty(1, dtype=torch.int32, device=self.device)
-        base = (self.pool.data_ptr() + 255) // 256 * 256
-        with torch.cuda.device(self.device):
-            self.c = dkv_kv4_init(self.desc, base, n_pages, self.status, stream)
         # what every call needs at hand: a decode step's calls take microseconds
         self._torch, self._lib, self._index = torch, load(), self.device.index
+        # the memory is taken where it is zeroed: a block that comes back from work
+        # still queued on another stream would be written under the zeroes
+        with self._elsewhere(stream) or contextlib.nullcontext():
+            self.pool = torch.empty(n_pages * pb + 256, dtype=torch.uint8, device=self.device)
+            self.status = torch.empty(1, dtype=torch.int32, device=self.device)
+            base = (self.pool.data_ptr() + 255) // 256 * 256
+            self.c = dkv_kv4_init(self.desc, base, n_pages, self.status)
         self._desc, self._pool = ctypes.byref(self.desc), ctypes.byref(self.c)
         self._codes = {torch.float32: DKV_F32, torch.float16: DKV_F16, torch.bfloat16: DKV_BF16}
         self._stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \

@@ -74,3 +74,23 @@ def test_values_that_no_query_sees_leave_every_bit(dkv_gpu, D, group, dtype, nq,
         rows = slice(first[b], first[b] + n)
         want = attention_of(kk[rows], vv[rows], q[b], group, n - nq + np.arange(nq), scale, window)
         R.check(got[1][0][b], got[1][1][b], want, dtype)
+
+
+def test_a_cache_made_on_another_stream(dkv_gpu):
+    """Its pages are zero although the current stream has a write to a block
+    of their size, given back already, still before it."""
+    H, page, n_pages = 8, 64, 400
+    size = n_pages * dkv_gpu.dkv_kv4_page_bytes(dkv_gpu.dkv_kv4_desc(H, 128, 32, page))
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        x = torch.empty(size + 256, dtype=torch.uint8, device="cuda")
+        torch.cuda._sleep(200_000_000)                 # about 0.1 s
+        x.fill_(255)
+        del x
+        cache = dkv_gpu.Kv4Cache(n_pages, H, page_size=page, stream=stream)
+        torch.cuda.synchronize()
+        base = cache.c.base - cache.pool.data_ptr()
+        assert not bool(cache.pool[base:base + size].any())
+        assert cache.device_status(stream=stream) == 0
+        del cache
