@@ -173,6 +173,16 @@ def _stream(s):
     return s.cuda_stream
 
 
+def _on(stream, device):
+    """A context in which torch allocates and launches on `stream` (None: as it does)."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device)
+    return torch.cuda.stream(stream)
+
+
 def _dtype_code(t) -> int:
     import torch
     return {torch.float32: DKV_F32, torch.float16: DKV_F16, torch.bfloat16: DKV_BF16}[t]
@@ -486,19 +496,23 @@ class Cache:
                 perm = torch.randperm(n_pages, generator=g)[:batch * max_pages]
                 block_table = perm.view(batch, max_pages).to(torch.int32)
             self.block_table = block_table.to(device=device, dtype=torch.int32).contiguous()
-            self.buf = torch.empty(mb + 256, dtype=torch.uint8, device=device)
-            self.pool = torch.empty(n_pages * pb + 256, dtype=torch.uint8, device=device)
-            base = (self.buf.data_ptr() + 255) // 256 * 256
-            pool = (self.pool.data_ptr() + 255) // 256 * 256
-            self.c = dkv_cache_init_paged(self.desc, page_groups, pool, n_pages,
-                                          self.block_table, max_pages, base, mb, stream)
         else:
             nbytes = dkv_cache_bytes(self.desc)
             if nbytes == 0:
                 raise DkvError(DKV_EINVAL, "dkv_cache_bytes")
-            self.buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+        # the memory is taken on the stream that initialises it: a block that comes
+        # back from work still queued on another one would be written under it
+        with _on(stream, device):
+            self.buf = torch.empty((mb if page_groups else nbytes) + 256, dtype=torch.uint8,
+                                   device=device)
             base = (self.buf.data_ptr() + 255) // 256 * 256
-            self.c = dkv_cache_init(self.desc, base, nbytes, stream)
+            if page_groups:
+                self.pool = torch.empty(n_pages * pb + 256, dtype=torch.uint8, device=device)
+                pool = (self.pool.data_ptr() + 255) // 256 * 256
+                self.c = dkv_cache_init_paged(self.desc, page_groups, pool, n_pages,
+                                              self.block_table, max_pages, base, mb)
+            else:
+                self.c = dkv_cache_init(self.desc, base, nbytes)
         self._ws = None
         self._ws_heads = None
         self.device = device
@@ -704,9 +718,7 @@ class Kv4Cache:
             if torch.cuda.current_device() == self._index:
                 return None
             return torch.cuda.device(self.device)
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, self.device)
-        return torch.cuda.stream(stream)
+        return _on(stream, self.device)
 
     # -- the operators ------------------------------------------------------
     def append(self, K_new, V_new, block_table, seq_lens, starts=None, stream=None):

@@ -94,3 +94,25 @@ def test_a_cache_made_on_another_stream(dkv_gpu):
         assert not bool(cache.pool[base:base + size].any())
         assert cache.device_status(stream=stream) == 0
         del cache
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_a_delta_cache_made_on_another_stream(dkv_gpu, paged):
+    kw = dict(page_groups=1) if paged else {}
+    plain = dkv_gpu.Cache(2, 2, 64, **kw)
+    k, v = torch.randn(2, 2, 2, 50, 128, device="cuda", dtype=F16)
+    q = torch.randn(2, 4, 128, device="cuda", dtype=F16)
+    plain.encode(k, v)
+    want = plain.decode_attn(q, 0.1)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        x = torch.empty(plain.buf.numel(), dtype=torch.uint8, device="cuda")
+        torch.cuda._sleep(200_000_000)                 # about 0.1 s
+        x.fill_(255)
+        del x
+        cache = dkv_gpu.Cache(2, 2, 64, stream=stream, **kw)
+        cache.encode(k, v, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(cache.decode_attn(q, 0.1), want)
+        assert cache.device_status() == 0

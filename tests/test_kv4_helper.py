@@ -1,5 +1,5 @@
-"""CPU checks of the Kv4Cache helper: what it does with streams, devices and
-arguments, on a torch.cuda and a library that only take notes."""
+"""CPU checks of the Kv4Cache helper (and of Cache's constructor): what they do with streams,
+devices and arguments, on a torch.cuda and a library that only take notes."""
 import contextlib
 from types import SimpleNamespace
 
@@ -53,3 +53,16 @@ def test_the_pool_is_taken_on_the_stream_that_zeroes_it(fake):
     fake.notes.clear()
     fake.dkv.Kv4Cache(3, 2, device="cuda:1")
     assert all(n[1:] == (1, "default") for n in fake.notes)
+
+
+def test_the_delta_caches_memory_too(fake, monkeypatch):
+    def init(desc, base, nbytes, stream=None):
+        fake.notes.append(("init", fake.device, fake.stream if stream is None else stream))
+        return fake.dkv.dkv_cache()
+
+    monkeypatch.setattr(fake.dkv, "dkv_cache_init", init)
+    for stream in (fake.side, None):
+        fake.notes.clear()
+        fake.dkv.Cache(1, 2, 64, device="cuda", stream=stream)
+        assert [n[0] for n in fake.notes] == ["empty", "init"]
+        assert all(n[1:] == (0, stream or "default") for n in fake.notes)
