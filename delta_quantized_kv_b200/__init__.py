@@ -84,7 +84,7 @@ EXPORTS = ["dkv_abi_version", "dkv_cache_bytes", "dkv_cache_init", "dkv_encode",
            "dkv_append_decode_attn", "dkv_append_decode_attn_split",
            "dkv_append_decode_attn_merge", "dkv_lr_encode", "dkv_lr_decode_workspace_bytes",
            "dkv_lr_decode_attn", "dkv_debug_division_check", "dkv_kv4_page_bytes",
-           "dkv_kv4_init", "dkv_kv4_append", "dkv_kv4_read", "dkv_kv4_decode_workspace_bytes",
+           "dkv_kv4_init", "dkv_kv4_get_device_status", "dkv_kv4_append", "dkv_kv4_read", "dkv_kv4_decode_workspace_bytes",
            "dkv_kv4_decode_attn", "dkv_kv4_prompt_workspace_bytes", "dkv_kv4_prompt_attn"]
 
 
@@ -136,6 +136,7 @@ def load():
                                 I, I, I, I, I, P, P, I, I, F, P, P, S, P], I),
         "dkv_kv4_page_bytes": ([D4], S),
         "dkv_kv4_init": ([D4, P, L, P, P4, P], I),
+        "dkv_kv4_get_device_status": ([P4, ctypes.POINTER(I), P], I),
         "dkv_kv4_append": ([P4, B4, P, P, I, I, L, L, L, L, P], I),
         "dkv_kv4_read": ([P4, B4, P, P, I, I, P], I),
         "dkv_kv4_decode_workspace_bytes": ([D4, I, I, I, I], S),
@@ -410,6 +411,14 @@ def dkv_kv4_init(desc: dkv_kv4_desc, pool, n_pages: int, status, stream=None) ->
     _check(load().dkv_kv4_init(ctypes.byref(desc), _ptr(pool), n_pages, _ptr(status),
                                ctypes.byref(out), _stream(stream)), "dkv_kv4_init")
     return out
+
+
+def dkv_kv4_get_device_status(pool: dkv_kv4_pool, stream=None) -> int:
+    word = ctypes.c_int32(0)
+    s = load().dkv_kv4_get_device_status(ctypes.byref(pool), ctypes.byref(word), _stream(stream))
+    if s not in (DKV_OK, DKV_EDEVICE):
+        raise DkvError(s, "dkv_kv4_get_device_status")
+    return word.value
 
 
 def dkv_kv4_append(pool: dkv_kv4_pool, seqs: dkv_kv4_batch, K, V, dtype, n_rows, k_row_stride,
@@ -836,12 +845,9 @@ class Kv4Cache:
                           n, seqs, softmax_scale, window, out, return_lse)
 
     def device_status(self, stream=None) -> int:
-        """Read and clear the pool's status word (synchronises)."""
+        """Read the pool's status word and clear what was read (synchronises)."""
         ctx = self._elsewhere(stream)
         if ctx is not None:
             with ctx:
                 return self.device_status()
-        word = int(self.status.item())
-        if word:
-            self.status.zero_()
-        return word
+        return dkv_kv4_get_device_status(self.c, self._stream(self._index))

@@ -13,6 +13,9 @@ namespace dkv {
 // launch: DKV_OK, or the status those entry points return for it.
 dkv_status validate_cache(const dkv_cache *c);
 
+// Synchronises the stream, reads the status word into *bits and clears those bits.
+cudaError_t take_status(int32_t *word, int32_t *bits, cudaStream_t st);
+
 // What dkv_debug_set_fault last set (test support).
 int debug_fault();
 

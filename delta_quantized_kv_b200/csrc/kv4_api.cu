@@ -143,6 +143,15 @@ dkv_status dkv_kv4_init(const dkv_kv4_desc *desc, void *pool, int64_t n_pages, i
     return cuda_status(e);
 }
 
+dkv_status dkv_kv4_get_device_status(const dkv_kv4_pool *pool, int32_t *host_out, void *stream) {
+    const dkv_status s = check_pool(pool);
+    if (s != DKV_OK) return s;
+    if (!host_out) return DKV_EINVAL;
+    if (dkv::take_status(pool->status, host_out, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return DKV_ECUDA;
+    return *host_out ? DKV_EDEVICE : DKV_OK;
+}
+
 dkv_status dkv_kv4_append(const dkv_kv4_pool *pool, const dkv_kv4_batch *seqs, const void *K,
                           const void *V, int32_t dtype, int32_t n_rows, int64_t k_row_stride,
                           int64_t k_head_stride, int64_t v_row_stride, int64_t v_head_stride,

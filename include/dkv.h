@@ -21,8 +21,8 @@
  *
  * Conventions for every entry point:
  *  - The caller owns all memory.  The library never allocates, never frees
- *    and never synchronises, except dkv_get_device_status (which synchronises
- *    the stream it is given).
+ *    and never synchronises, except dkv_get_device_status and
+ *    dkv_kv4_get_device_status (which synchronise the stream they are given).
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *    stream).  Every call is asynchronous on that stream.  The append,
  *    decode-split and merge kernels, and the long-range decode's kernels, are
@@ -51,7 +51,7 @@
 extern "C" {
 #endif
 
-#define DKV_ABI_VERSION 4
+#define DKV_ABI_VERSION 5
 
 typedef enum {
     DKV_OK = 0,
@@ -347,7 +347,8 @@ dkv_status dkv_lr_decode_attn(const dkv_lr_tensor *K, const dkv_lr_tensor *V, in
  *    position seq_lens[b] - n_b + i, so seq_lens counts the rows' own tokens.
  *    Rows at or behind starts[batch] are padding: never read, never written.
  *    A sequence may have no rows, and length 0.
- *  - Faults found on the device set bits of the pool's status word.
+ *  - Faults found on the device set bits of the pool's status word
+ *    (dkv_kv4_get_device_status reads and clears it).
  *    DKV_DEV_BAD_SEQLEN: a length outside [0, max_pages * page_size], or a
  *    sequence with more rows than positions (its rows are skipped: not stored,
  *    outputs left as they were; dkv_kv4_decode_attn treats a bad length as 0);
@@ -395,6 +396,11 @@ size_t dkv_kv4_page_bytes(const dkv_kv4_desc *desc);
  * Zeroes both with cudaMemsetAsync on `stream` (zeroed pages hold zeros). */
 dkv_status dkv_kv4_init(const dkv_kv4_desc *desc, void *pool, int64_t n_pages, int32_t *status,
                         dkv_kv4_pool *out, void *stream);
+
+/* Synchronise `stream`, copy the pool's status word to *host_out and clear the
+ * bits that were read (a fault that a call on another stream reports meanwhile
+ * stays for the next time).  Returns DKV_EDEVICE if the word was not zero. */
+dkv_status dkv_kv4_get_device_status(const dkv_kv4_pool *pool, int32_t *host_out, void *stream);
 
 /* Quantise n_rows rows of keys and values, as they are written, into the pages
  * of their sequences.  K, V: row i, kv head h at i * row_stride + h *

@@ -116,3 +116,29 @@ def test_a_delta_cache_made_on_another_stream(dkv_gpu, paged):
         torch.cuda.synchronize()
         assert torch.equal(cache.decode_attn(q, 0.1), want)
         assert cache.device_status() == 0
+
+
+def test_every_fault_is_reported(dkv_gpu):
+    """Calls with bad lengths and bad pages on one stream, status reads on
+    another meanwhile: no report is lost."""
+    d = dkv_gpu
+    cache, table, end, _, _ = fill(d, [40, 20], 1, 64, 32, 16, F16, 1)
+    q = torch.randn(2, 1, 64, device="cuda", dtype=F16)
+    bad_page, bad_len = table.clone(), end.clone()
+    bad_page[0, 0], bad_len[1] = 10 ** 6, -1
+    side, done = torch.cuda.Stream(), torch.cuda.Event()
+    rng = np.random.default_rng(1)
+    for i in range(100):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(int(rng.integers(0, 100_000)))
+            cache.decode_attn(q, 0.1, bad_page, end)
+            torch.cuda._sleep(int(rng.integers(0, 50_000)))
+            cache.decode_attn(q, 0.1, table, bad_len)
+            done.record()
+        got, last = 0, False
+        while not last:
+            last = done.query()
+            got |= cache.device_status()
+        assert got == d.DEV_BAD_PAGE | d.DEV_BAD_SEQLEN, i
+    assert cache.device_status() == 0 and int(cache.status.item()) == 0

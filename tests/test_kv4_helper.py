@@ -66,3 +66,37 @@ def test_the_delta_caches_memory_too(fake, monkeypatch):
         fake.dkv.Cache(1, 2, 64, device="cuda", stream=stream)
         assert [n[0] for n in fake.notes] == ["empty", "init"]
         assert all(n[1:] == (0, stream or "default") for n in fake.notes)
+
+
+def test_a_fault_reported_while_the_status_is_read_is_not_lost(fake, monkeypatch):
+    word = [0x1]
+
+    def read(*_):                     # another stream reports 0x10 right behind the read
+        seen = word[0]
+        word[0] |= 0x10
+        return seen
+
+    def library(pool, stream=None):   # clears what it read
+        seen = read()
+        word[0] &= ~seen
+        return seen
+
+    cache = fake.dkv.Kv4Cache(3, 2, device="cuda:0")
+    cache._stream = lambda index: 0
+    cache.status = SimpleNamespace(item=read, zero_=lambda: word.__setitem__(0, 0))
+    monkeypatch.setattr(fake.dkv, "dkv_kv4_get_device_status", library, raising=False)
+    assert cache.device_status() == 0x1
+    assert cache.device_status() & 0x10
+
+
+def test_refused_status_reads(fake):
+    import ctypes
+    d, lib, b = fake.dkv, fake.dkv.load(), ctypes.byref
+    word, P = ctypes.c_int32(5), 1 << 20
+    desc = d.dkv_kv4_desc(2, 128, 32, 64)
+    nb = d.dkv_kv4_page_bytes(desc)
+    for pool, out, want in ((None, b(word), d.DKV_EINVAL), (d.dkv_kv4_pool(desc, P, 4, nb, P), None, d.DKV_EINVAL),
+                            (d.dkv_kv4_pool(desc, P, 4, nb, None), b(word), d.DKV_EINVAL),
+                            (d.dkv_kv4_pool(desc, P, 4, nb, P + 2), b(word), d.DKV_EALIGN)):
+        assert lib.dkv_kv4_get_device_status(None if pool is None else b(pool), out, 0) == want
+        assert word.value == 5
