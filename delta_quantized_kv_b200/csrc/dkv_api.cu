@@ -474,16 +474,10 @@ dkv_status dkv_get_device_status(const dkv_cache *cache, int32_t *host_out, void
     dkv_status s = check_cache(cache);
     if (s != DKV_OK) return s;
     if (!host_out) return DKV_EINVAL;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     int32_t *word = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(cache->base) + cache->off_header);
-    int32_t h = 0;
-    cudaError_t e = cudaMemcpyAsync(&h, word, sizeof(h), cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof(int32_t), st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess) return DKV_ECUDA;
-    *host_out = h;
-    return h ? DKV_EDEVICE : DKV_OK;
+    if (dkv::take_status(word, host_out, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return DKV_ECUDA;
+    return *host_out ? DKV_EDEVICE : DKV_OK;
 }
 
 void dkv_debug_set_fault(int32_t mode) { g_debug_fault = (mode == 1 || mode == 2) ? mode : 0; }

@@ -498,8 +498,8 @@ dkv_status dkv_export_canonical(const dkv_cache *cache, uint8_t *codes, uint16_t
  * [B][Hkv][2][max_ctx][D] (positions >= seq_len are left untouched). */
 dkv_status dkv_dequantize(const dkv_cache *cache, float *out, void *stream);
 
-/* Synchronise `stream`, copy the device status word to *host_out and clear
- * it.  Returns DKV_EDEVICE if it was non-zero, DKV_OK otherwise. */
+/* Synchronise `stream`, copy the device status word to *host_out and clear the
+ * bits that were read.  Returns DKV_EDEVICE if it was non-zero, DKV_OK otherwise. */
 dkv_status dkv_get_device_status(const dkv_cache *cache, int32_t *host_out, void *stream);
 
 /* Test support for failure detection (no counterpart on the pages).  With

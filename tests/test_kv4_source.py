@@ -24,3 +24,13 @@ def test_a_warp_gives_up_a_wait_together(name):
     vote = "__all_sync(0xffffffffu, "
     assert all(s[:i].endswith(vote) for i in waits)
     assert bool(waits) == (name == "kv4_common.cuh")
+
+
+@pytest.mark.parametrize("name", ["dkv_api.cu", "kv4_api.cu"])
+def test_status_words_are_cleared_of_what_was_read(name):
+    """Both caches' status reads go through the one that clears bits atomically."""
+    s = code(name)
+    body = s[s.index("get_device_status("):]
+    body = body[:body.index("\n}\n")]
+    assert "take_status(" in body and "Memset" not in body and "Memcpy" not in body
+    assert "atomicAnd(word, ~bits)" in code("status.cu")
