@@ -34,3 +34,9 @@ def test_status_words_are_cleared_of_what_was_read(name):
     body = body[:body.index("\n}\n")]
     assert "take_status(" in body and "Memset" not in body and "Memcpy" not in body
     assert "atomicAnd(word, ~bits)" in code("status.cu")
+
+
+def test_every_source_is_built():
+    from delta_quantized_kv_b200 import build
+    assert sorted(p.name for p in CSRC.glob("*.cu")) == sorted(build.SOURCES)
+    assert sorted(p.name for p in CSRC.iterdir() if p.suffix in (".cuh", ".h")) == sorted(build.HEADERS)
