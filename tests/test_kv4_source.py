@@ -40,3 +40,20 @@ def test_every_source_is_built():
     from delta_quantized_kv_b200 import build
     assert sorted(p.name for p in CSRC.glob("*.cu")) == sorted(build.SOURCES)
     assert sorted(p.name for p in CSRC.iterdir() if p.suffix in (".cuh", ".h")) == sorted(build.HEADERS)
+
+
+def test_the_runs_test_has_the_kernels_constants():
+    """test_kv4_host.py restates the formulas that cut a prompt call into runs."""
+    import test_kv4_host as host
+    s = code("kv4_prompt.cu")
+    for name in ("TM", "TN", "COST", "MIN_TILES"):
+        assert int(re.search(rf"constexpr int {name} = (\d+);", s).group(1)) == getattr(host, name)
+    # and the formulas themselves, line for line
+    for line in ("const int64_t k = u.full <= u.base ? 0 : min(m, (u.full - u.base) / (2 * TM));",
+                 "return u.base * k + TM * k * (k + 1) + (m > k ? (m - k) * u.full : 0) + m * u.cost;",
+                 "return min(u.full, u.base + 2 * TM * (m + 1)) + u.cost;",
+                 "u.full = p.q.window > 0 ? (int64_t)p.G * p.q.window + 2 * TM : INT64_MAX;",
+                 "u.cost = (int64_t)COST * TN * p.G;",
+                 "const int64_t least = (int64_t)MIN_TILES * TN * G, n = total / least;",
+                 "const int64_t each = (units - u.cost + tiles - 1) / tiles;"):
+        assert line in s, line
