@@ -690,12 +690,14 @@ class Kv4Cache:
 
     def _batch(self, block_table, seq_lens, starts):
         i32, dev = self._torch.int32, self._index
-        for x, dims in ((block_table, 2), (seq_lens, 1), (starts, 1)):
-            if x is None and x is starts:
-                continue
+        for name, x, dims in (("block_table", block_table, 2), ("seq_lens", seq_lens, 1),
+                              ("starts", starts, 1)):
+            if x is None:
+                if name == "starts":
+                    continue
+                raise ValueError(f"{name} is missing")
             if x.get_device() != dev or x.dim() != dims or x.dtype is not i32 \
                     or not x.is_contiguous():
-                name = "block_table" if dims == 2 else "seq_lens" if x is seq_lens else "starts"
                 self._tensor(x, name, dims)
                 raise ValueError(f"{name} must be contiguous int32")
         (B,), (rows, width) = seq_lens.shape, block_table.shape

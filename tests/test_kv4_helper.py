@@ -100,3 +100,14 @@ def test_refused_status_reads(fake):
                             (d.dkv_kv4_pool(desc, P, 4, nb, P + 2), b(word), d.DKV_EALIGN)):
         assert lib.dkv_kv4_get_device_status(None if pool is None else b(pool), out, 0) == want
         assert word.value == 5
+
+
+def test_a_missing_table_or_length_is_refused(fake):
+    cache = fake.dkv.Kv4Cache(3, 2, device="cuda:0")
+    q = torch.zeros(1, 4, 128, dtype=torch.float16)
+    on = SimpleNamespace(get_device=lambda: 0, dim=lambda: 2, dtype=torch.int32, is_contiguous=lambda: True, shape=(1, 3))
+    for table in (None, on):
+        for call in (lambda: cache.read(2, table, None), lambda: cache.decode_attn(q, 0.1, table, None),
+                     lambda: cache.prompt_attn(q, 0.1, table, None)):
+            with pytest.raises(ValueError, match="seq_lens" if table else "block_table"):
+                call()
