@@ -729,6 +729,8 @@ class Kv4Cache:
             if torch.cuda.current_device() == self._index:
                 return None
             return torch.cuda.device(self.device)
+        if not isinstance(stream, int) and stream.device != self.device:
+            raise ValueError(f"the stream is of {stream.device}, the cache on {self.device}")
         return _on(stream, self.device)
 
     # -- the operators ------------------------------------------------------

@@ -111,3 +111,18 @@ def test_a_missing_table_or_length_is_refused(fake):
                      lambda: cache.prompt_attn(q, 0.1, table, None)):
             with pytest.raises(ValueError, match="seq_lens" if table else "block_table"):
                 call()
+
+
+def test_a_stream_of_another_device_is_refused(fake):
+    """A call on it would go to a stream that the caller does not know."""
+    cache = fake.dkv.Kv4Cache(3, 2, device="cuda:0")
+    other = SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=78)
+    q = torch.zeros(1, 4, 128, dtype=torch.float16)
+    for call in (lambda: cache.append(q, q, None, None, stream=other), lambda: cache.read(1, None, None, stream=other),
+                 lambda: cache.decode_attn(q, 0.1, None, None, stream=other),
+                 lambda: cache.prompt_attn(q, 0.1, None, None, stream=other),
+                 lambda: cache.device_status(stream=other),
+                 lambda: fake.dkv.Kv4Cache(3, 2, device="cuda:0", stream=other)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
+    assert (fake.device, fake.stream) == (0, "default")
