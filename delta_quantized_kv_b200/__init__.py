@@ -764,15 +764,17 @@ class Kv4Cache:
         torch = self._torch
         shape = (n_rows, self.desc.n_kv_heads, self.desc.head_dim)
         seqs = self._batch(block_table, seq_lens, starts)
+        if dtype is None:
+            dtype = torch.float16 if out is None else out[0].dtype
+        if dtype not in self._codes:
+            raise ValueError(f"dtype is {dtype}, not fp32, fp16 or bf16")
         if out is None:
-            dtype = torch.float16 if dtype is None else dtype
             k = self.status.new_empty(shape, dtype=dtype)
             out = (k, torch.empty_like(k))
         else:
             for x in out:
                 self._tensor(x, "out")
-                if tuple(x.shape) != shape or not x.is_contiguous() or x.dtype != out[0].dtype \
-                        or (dtype is not None and x.dtype != dtype):
+                if tuple(x.shape) != shape or not x.is_contiguous() or x.dtype != dtype:
                     raise ValueError("out must be two contiguous tensors [n_rows, n_kv_heads, "
                                      "head_dim] of dtype")
         k, v = out

@@ -126,3 +126,36 @@ def test_a_stream_of_another_device_is_refused(fake):
         with pytest.raises(ValueError, match="stream"):
             call()
     assert (fake.device, fake.stream) == (0, "default")
+
+
+@pytest.fixture
+def on_cpu(fake):
+    """A cache whose tensors are the CPU's, with a library that notes the
+    arguments of its calls."""
+    cache = fake.dkv.Kv4Cache(3, 2, device="cuda:0")
+    cache.device, cache._index, fake.device = torch.device("cpu"), -1, -1
+    cache._stream = lambda index: 0
+    cache.calls = []
+
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                cache.calls.append((name, args))
+                return 64 if name.endswith("_bytes") else 0
+            return call
+
+    cache._lib = Library()
+    cache.table, cache.lens = torch.zeros((2, 3), dtype=torch.int32), torch.tensor([5, 7], dtype=torch.int32)
+    return cache
+
+
+def test_types_that_read_does_not_give_are_refused(on_cpu):
+    c = on_cpu
+    two = (torch.zeros(2, 2, 128, dtype=torch.float64), torch.zeros(2, 2, 128, dtype=torch.float64))
+    for kw in (dict(dtype=torch.float64), dict(dtype=torch.int8), dict(out=two), dict(out=two, dtype=torch.float64)):
+        for n in (2, 0):
+            with pytest.raises(ValueError):
+                c.read(n, c.table, c.lens, **{**kw, **({"out": tuple(x[:n] for x in two)} if "out" in kw else {})})
+    assert not c.calls
+    assert c.read(2, c.table, c.lens)[0].dtype == torch.float16
+    assert c.read(0, c.table, c.lens, dtype=torch.bfloat16)[1].dtype == torch.bfloat16
