@@ -27,6 +27,7 @@ DKV_FMT_FP16, DKV_FMT_Q4_0, DKV_FMT_DELTA = 0, 1, 2
 DKV_F32, DKV_F16, DKV_BF16 = 0, 1, 2
 DEV_BAD_SEQLEN, DEV_CAPACITY, DEV_TIMEOUT, DEV_BAD_HEADS, DEV_BAD_PAGE = 0x1, 0x2, 0x4, 0x8, 0x10
 DEV_BOUNDS = 0x20
+_I32_MAX = 2 ** 31 - 1      # ctypes drops what a C int32 has no room for
 FORMATS = {"fp16": DKV_FMT_FP16, "q4": DKV_FMT_Q4_0, "delta": DKV_FMT_DELTA}
 
 
@@ -657,9 +658,11 @@ class Kv4Cache:
     def __init__(self, n_pages, n_kv_heads, head_dim=128, page_size=64, group=32, device="cuda",
                  stream=None):
         import torch
-        self.desc = dkv_kv4_desc(n_kv_heads, head_dim, group, page_size)
+        given = (n_kv_heads, head_dim, group, page_size)
+        self.desc = dkv_kv4_desc(*given)
         pb = dkv_kv4_page_bytes(self.desc)
-        if pb == 0 or n_pages < 1:
+        kept = tuple(getattr(self.desc, name) for name, _ in self.desc._fields_)
+        if pb == 0 or n_pages < 1 or kept != given:
             raise DkvError(DKV_EINVAL, "dkv_kv4_page_bytes")
         self.device = torch.device(device)
         if self.device.type != "cuda":
@@ -701,6 +704,8 @@ class Kv4Cache:
                 self._tensor(x, name, dims)
                 raise ValueError(f"{name} must be contiguous int32")
         (B,), (rows, width) = seq_lens.shape, block_table.shape
+        if width > _I32_MAX:
+            raise ValueError(f"block_table has {width} columns")
         if rows != B or (starts is not None and starts.shape[0] != B + 1):
             raise ValueError("block_table, seq_lens and starts disagree about the batch")
         return dkv_kv4_batch(B, width, block_table.data_ptr(), seq_lens.data_ptr(),
@@ -712,7 +717,8 @@ class Kv4Cache:
         if x.get_device() != self._index or x.dim() != 3:
             self._tensor(x, name, 3)
         shape, (row, head, one) = x.shape, x.stride()
-        if shape[2] != self.desc.head_dim or (heads is not None and shape[1] != heads):
+        if shape[2] != self.desc.head_dim or (heads is not None and shape[1] != heads) \
+                or shape[0] > _I32_MAX:
             raise ValueError(f"{name} has shape {tuple(shape)}")
         if one != 1:
             raise ValueError(f"{name} must have contiguous channels")
@@ -802,6 +808,8 @@ class Kv4Cache:
             size, call = (lib.dkv_kv4_decode_workspace_bytes, lib.dkv_kv4_decode_attn) \
                 if what == "decode" else (lib.dkv_kv4_prompt_workspace_bytes, lib.dkv_kv4_prompt_attn)
             nb = size(self._desc, *sizes)
+            # a window past every position counts as none: it need not fit 32 bits
+            window = max(-1, min(window, _I32_MAX))
             ws = self.status.new_empty(nb // 4 + 4)
             _check(call(self._pool, ctypes.byref(seqs), rows.data_ptr(), code, shape[1], n_queries,
                      row, head, softmax_scale, window, out.data_ptr(),

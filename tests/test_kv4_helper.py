@@ -159,3 +159,36 @@ def test_types_that_read_does_not_give_are_refused(on_cpu):
     assert not c.calls
     assert c.read(2, c.table, c.lens)[0].dtype == torch.float16
     assert c.read(0, c.table, c.lens, dtype=torch.bfloat16)[1].dtype == torch.bfloat16
+
+
+def test_numbers_past_32_bits_are_refused_or_kept(on_cpu, fake):
+    """The library's counts and windows have 32 bits; what passes them must not
+    come out as something else."""
+    import ctypes
+    c = on_cpu
+    q = torch.zeros(2, 4, 128, dtype=torch.float16)
+    for window in (2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63):
+        for f in (c.decode_attn, c.prompt_attn):
+            c.calls.clear()
+            f(q, 0.1, c.table, c.lens, window=window)
+            got = c.calls[-1][1][9]                     # past every position: as none
+            assert ctypes.c_int32(got).value == got and got > 1 << 30
+    for window in (-1, -2 ** 31, -2 ** 32, -2 ** 32 - 5):
+        for f in (c.decode_attn, c.prompt_attn):
+            c.calls.clear()
+            f(q, 0.1, c.table, c.lens, window=window)   # (the library refuses it)
+            assert ctypes.c_int32(c.calls[-1][1][9]).value < 0
+    c.calls.clear()
+    k = torch.zeros((1, 2, 128), dtype=torch.float16).expand(2 ** 32 + 2, 2, 128)
+    table = SimpleNamespace(get_device=lambda: -1, dim=lambda: 2, dtype=torch.int32, is_contiguous=lambda: True,
+                            shape=(2, 2 ** 32 + 3), data_ptr=lambda: 256)
+    with pytest.raises(ValueError):
+        c.append(k, k, c.table, c.lens)
+    with pytest.raises(ValueError):
+        c.append(q[:, :2], q[:, :2], table, c.lens)
+    for bad in (dict(n_kv_heads=2 ** 32 + 2), dict(head_dim=128 - 2 ** 32), dict(group=2 ** 32 + 32),
+                dict(page_size=2 ** 32 + 64)):
+        with pytest.raises(fake.dkv.DkvError):
+            fake.dkv.Kv4Cache(3, **{"n_kv_heads": 2, "device": "cuda:0", **bad})
+    assert not c.calls
+
