@@ -159,8 +159,9 @@ __device__ inline uint32_t encode8(const float (&x)[8], const Block &b) {
 }
 
 // Record of `token` (head 0's; one head's pages are `head` bytes apart) and its
-// place *tok there; nullptr if the token is to be skipped (behind the last
-// sequence, a bad length, a bad page).  *b: a sequence at or before the token's.
+// place *tok there; nullptr if the token is to be skipped (before the first
+// sequence or behind the last, a bad length, a bad page).  *b: a sequence at or
+// before the token's.
 __device__ inline uint8_t *token_record(const View &v, int token, int *b, int rec, int *tok) {
     if (v.starts) {
         while (*b < v.B && v.starts[*b + 1] <= token) ++*b;
@@ -169,10 +170,7 @@ __device__ inline uint8_t *token_record(const View &v, int token, int *b, int re
     }
     if (*b >= v.B) return nullptr;
     const int s0 = seq_start(v, *b), n = (v.starts ? v.starts[*b + 1] : s0 + v.n_uniform) - s0;
-    if (token < s0 || s0 < 0) {            // starts decrease, or begin behind a row
-        set_status(v.status, DKV_DEV_BAD_SEQLEN);
-        return nullptr;
-    }
+    if (token < s0 || s0 < 0) return nullptr;      // before starts[0], or starts decrease
     const int len = seq_len(v, *b);
     if (len < 0) return nullptr;
     if (n > len) {                         // more rows than positions

@@ -346,6 +346,7 @@ dkv_status dkv_lr_decode_attn(const dkv_lr_tensor *K, const dkv_lr_tensor *V, in
  *    (starts NULL: n_rows / batch rows each); row i of the n_b rows stands for
  *    position seq_lens[b] - n_b + i, so seq_lens counts the rows' own tokens.
  *    Rows at or behind starts[batch] are padding: never read, never written.
+ *    Rows before starts[0] belong to no sequence either: not used, not written.
  *    A sequence may have no rows, and length 0.
  *  - Faults found on the device set bits of the pool's status word
  *    (dkv_kv4_get_device_status reads and clears it).

@@ -142,3 +142,24 @@ def test_every_fault_is_reported(dkv_gpu):
             got |= cache.device_status()
         assert got == d.DEV_BAD_PAGE | d.DEV_BAD_SEQLEN, i
     assert cache.device_status() == 0 and int(cache.status.item()) == 0
+
+
+def test_rows_before_the_first_sequence_are_padding(dkv_gpu):
+    """starts[0] > 0: such rows are passed over, and are no fault."""
+    cache, table, end, _, _ = fill(dkv_gpu, [40, 20], 2, 64, 32, 16, F16, 1)
+    k = torch.randn(12, 2, 64, device="cuda", dtype=F16)
+    starts = torch.tensor([4, 7, 10], dtype=torch.int32, device="cuda")
+    cache.append(k, k, table, end, starts)
+    assert cache.device_status() == 0
+    out = tuple(torch.full((12, 2, 64), -5.0, device="cuda", dtype=F32) for _ in range(2))
+    cache.read(12, table, end, starts, out=out)
+    assert cache.device_status() == 0
+    for y in out:
+        assert np.array_equal(y[4:10].cpu().numpy(), R.held(k[4:10].float().cpu().numpy(), 32).astype(np.float32))
+        assert bool((y[:4] == -5).all()) and bool((y[10:] == -5).all())
+    q = torch.randn(12, 4, 64, device="cuda", dtype=F16)
+    a, b = torch.full_like(q, -5), torch.full_like(q[4:10], -5)
+    cache.prompt_attn(q, 0.1, table, end, starts, out=a)
+    cache.prompt_attn(q[4:10], 0.1, table, end, starts - 4, out=b)
+    assert torch.equal(a[4:10], b) and bool((a[:4] == -5).all()) and bool((a[10:] == -5).all())
+    assert cache.device_status() == 0
