@@ -646,6 +646,8 @@ prompt_kernel(View v, Prompt p) {
                         u[i] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
+                // not 0: hidden scores are -inf, and 0 times that is NaN
+                c1 = fmaxf(c1, 1.17549435e-38f);
 #pragma unroll
                 for (int i = 0; i < L::D / 8; ++i)
                     *reinterpret_cast<uint4 *>(qrow + (i >> 3) * (128 * 128) +

@@ -163,3 +163,23 @@ def test_rows_before_the_first_sequence_are_padding(dkv_gpu):
     cache.prompt_attn(q[4:10], 0.1, table, end, starts - 4, out=b)
     assert torch.equal(a[4:10], b) and bool((a[:4] == -5).all()) and bool((a[10:] == -5).all())
     assert cache.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,scale,gain", [(F16, 1e-44, 1.0), (BF16, 1e-44, 1.0), (BF16, 1e-10, 1e-34),
+                                              (F16, 1e-30, 1e-4)])
+def test_scores_too_small_for_a_float(dkv_gpu, dtype, scale, gain):
+    """All weights are the same: the mean of the values seen."""
+    lens, new, H, D = [300, 40], [150, 9], 1, 64
+    cache, table, end, ks, vs = fill(dkv_gpu, lens, H, D, 32, 16, dtype, 3)
+    q = (torch.randn(sum(new), 2, D, device="cuda") * gain).to(dtype)
+    out, lse = cache.prompt_attn(q, scale, table, end, R.starts_of(new), return_lse=True)
+    last = torch.stack([q[new[0] - 1], q[-1]])
+    one, lse_one = cache.decode_attn(last, scale, table, end, return_lse=True)
+    assert cache.device_status() == 0
+    row = 0
+    for b, n in enumerate(lens):
+        pos = n - new[b] + np.arange(new[b])
+        rows = slice(row, row + new[b])
+        R.check(out[rows], lse[rows], attention_of(ks[b], vs[b], q[rows], 32, pos, scale, 0), dtype, exact_values=True)
+        R.check(one[b:b + 1], lse_one[b:b + 1], attention_of(ks[b], vs[b], last[b:b + 1], 32, pos[-1:], scale, 0), dtype)
+        row += new[b]
