@@ -23,6 +23,7 @@ inline bool valid_scale(float s) { return s > 0.f && s < 1e30f; }   // finite, >
 constexpr int32_t kMaxQueries = 16;
 constexpr int64_t kMaxPositions = (int64_t)1 << 30;
 constexpr int64_t kMaxRows = (int64_t)1 << 33;       // rows x kv heads: grids stay in range
+constexpr int32_t kMaxTokens = INT32_MAX - 1023;     // a row's number and a warp's share, summed
 constexpr int64_t kMaxQueryRows = (int64_t)1 << 30;  // prompt: rows x query heads
 constexpr int64_t kMaxRuns = (int64_t)1 << 24;       // decode: batch x kv heads x head groups
 
@@ -70,7 +71,8 @@ dkv_status make_view(const dkv_kv4_pool *p, const dkv_kv4_batch *b, int32_t n_ro
     if (s != DKV_OK) return s;
     const int32_t *starts = ragged ? b->starts : nullptr;
     if (!starts && n_rows % b->batch != 0) return DKV_EINVAL;
-    if ((int64_t)n_rows * p->desc.n_kv_heads > kMaxRows) return DKV_ECAPACITY;
+    if (n_rows > kMaxTokens || (int64_t)n_rows * p->desc.n_kv_heads > kMaxRows)
+        return DKV_ECAPACITY;
     if (!aligned(b->block_table, 4) || !aligned(b->seq_lens, 4) || !aligned(starts, 4))
         return DKV_EALIGN;
     v->pool = static_cast<uint8_t *>(p->base);

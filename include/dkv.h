@@ -406,7 +406,8 @@ dkv_status dkv_kv4_get_device_status(const dkv_kv4_pool *pool, int32_t *host_out
 /* Quantise n_rows rows of keys and values, as they are written, into the pages
  * of their sequences.  K, V: row i, kv head h at i * row_stride + h *
  * head_stride elements of `dtype` (any of the three).  All inputs are taken
- * (the block rule clamps; NaN becomes 0). */
+ * (the block rule clamps; NaN becomes 0).  n_rows <= 2^31 - 1024 and n_rows *
+ * n_kv_heads <= 2^33, here and in dkv_kv4_read. */
 dkv_status dkv_kv4_append(const dkv_kv4_pool *pool, const dkv_kv4_batch *seqs, const void *K,
                           const void *V, int32_t dtype, int32_t n_rows, int64_t k_row_stride,
                           int64_t k_head_stride, int64_t v_row_stride, int64_t v_head_stride,
