@@ -27,6 +27,13 @@ def test_large_pages(dkv_gpu, page, D, group, dtype):
     prompt_case(dkv_gpu, lens, new, 2, 3, D, group, page, dtype, window=131, seed=page, every=9)
 
 
+@pytest.mark.parametrize("G", [40, 300, 1024])
+def test_many_query_heads_of_one_kv_head(dkv_gpu, G):
+    decode_case(dkv_gpu, [130, 3, 0], 1, G, 64, 32, 16, BF16, 2, 0, seed=G)
+    prompt_case(dkv_gpu, [400, 33, 5], [9, 33, 0], 1, G, 64, 32, 16, BF16, seed=G, pad=1, every=4)
+    prompt_case(dkv_gpu, [400, 33, 5], [9, 33, 0], 1, G, 64, 32, 16, F16, window=50, seed=G, every=4)
+
+
 def test_sixteen_thousand_sequences(dkv_gpu):
     B, H, G, D, page = 16384, 2, 2, 64, 16
     rng = np.random.default_rng(1)
