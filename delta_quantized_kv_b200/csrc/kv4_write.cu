@@ -372,10 +372,16 @@ read_kernel(View v, void *K, void *V, int per_warp, int heads) {
     }
 }
 
-// A warp's share: one row of each of its lanes while that leaves SMs idle, all
-// heads of a token in longer calls, and of 4 tokens in long ones (the token's
-// place is found once for them).  64 tokens of 8 heads written and read: 5.9 us
-// with a row each, 7.6 us with all heads.
+// A warp's share: one row of each of its lanes while such warps are fewer than
+// 2048, all heads of a token in longer calls, and of 2 or 4 tokens in long ones
+// (the token's place is found once for them).  us of an append / a read of N
+// tokens of 8 heads (D 128, bf16) with a row each, and all heads of 1, 2, 4 tokens:
+//   256: 2.9/2.6, 3.7/2.9, -, -        512: 3.8/3.7, 3.7/2.8, 5.7/4.1, -
+//  1024: 5.7/5.1, 4.3/3.5, 5.7/4.1, -  4096: 18.4/14.5, 9.4/6.3, 10.2/7.6, 11.9/8.4
+//  8192: -, 16.8/10.6, 16.4/10.4, 18.6/13.1
+// 16384: -, 31.9/19.7, 30.9/18.2, 31.3/18.6
+// 65536: -, 122/80.6, 117/71.9, 116/70.8
+// and of 8 heads of D 64 in fp32: 512: 2.9/2.9, 3.1/2.9; 1024: 4.9/3.8, 3.4/3.4.
 struct Share {
     int tokens, heads;
     dim3 grid;
@@ -385,7 +391,7 @@ Share share_of(const View &v) {
     constexpr int RW = 32 / (L::D / 8);
     Share s;
     s.tokens = v.n_rows < 8192 ? 1 : v.n_rows < 16384 ? 2 : 4;
-    s.heads = (int64_t)v.n_rows * v.H < 16384 ? RW : v.H;
+    s.heads = (int64_t)v.n_rows * v.H < 2048 * RW ? RW : v.H;
     const int64_t per = (int64_t)WARPS * s.tokens;
     s.grid = dim3((unsigned)((v.n_rows + per - 1) / per), 2, (v.H + s.heads - 1) / s.heads);
     return s;
