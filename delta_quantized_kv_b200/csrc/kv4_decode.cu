@@ -12,9 +12,10 @@
 // joins them.
 //
 // Measured on one B200: 16 sequences of 32768 positions, 64 heads over 8, D 128,
-// bf16: 163 us, 3.7 TB/s of packed cache.  Bound by instructions, not by DRAM:
-// 774 a unit, 60 % of the issue slots and of the ALU's (masks and shifts of the
-// codes), the tensor cores at 22 %.
+// bf16: 163 us, 3.7 TB/s of packed cache.  Bound by latency: a unit is one chain
+// (scores, maximum, vote, exponentials, products), and 3.7 warps a scheduler fill
+// 56 % of the issue slots (860 instructions a unit at 8192 positions a sequence),
+// the ALU 54 % (masks and shifts of the codes), the tensor cores 19 %, DRAM 44 %.
 //
 // Mathematics.  x^ = (c - z) s, so with the sum over a block's channels
 //   q . k^ = sum_b s_b (q_b . c_b) + sum_b (s_b z_b) (-sum q_b):

@@ -27,11 +27,12 @@
 // by more than 8 since ref was set, so it seldom is.  Weights in [.., 2^15]
 // are rounded to fp16 once; sums and scores are fp32.
 //
-// Measured on one B200: a prompt of 8192 tokens (32 heads over 8, D 128, bf16)
-// 606-630 us, 870-910 TFLOP/s; chunks of 500 and 160 tokens behind 24577 and
-// 13187 positions 255 us, 0.93 PFLOP/s.  A CTA takes 4100-4500 clocks for two
-// query tiles and 128 positions; the softmax warps are at work for 90 % of
-// them, the tensor cores for 2048.
+// Measured on one B200: a prompt of 8192 tokens (32 heads over 8, D 128, bf16) in
+// 653 us a call, 840 TFLOP/s (calls queued behind one another: 610-622); chunks of
+// 500 and 160 tokens behind 24577 and 13187 positions in 278 us, 860 TFLOP/s
+// (259-261).  A CTA takes 4100-4500 clocks for two query tiles and 128 positions;
+// the softmax warps are at work for 90 % of them, the tensor cores for 44 %; ALU
+// and exponentials are at 45 %, the issue slots at 55 %.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -261,7 +262,10 @@ __device__ inline int q_exponent(float mx) {
 // The units of the batch are cut into equal runs, one per CTA: a run may begin
 // and end inside a job, and has its position tiles from and up to there.
 // ---------------------------------------------------------------------------
-constexpr int COST = 3;            // (a prompt of 8192 with 3: 653 us; with 1, 2, 5: 750, 693, 652)
+// us with 1, 2, 3, 4, 5 (calls queued): a prompt of 8192 708, 657, 615, 604, 609; 24
+// short windowed prompts 79.7, 80.0, 82.1, 83.1, 83.9; a chunk behind a long prefix the
+// same with all
+constexpr int COST = 3;
 constexpr int MIN_TILES = 6;       // of a run, where there are enough
 
 struct Seq {

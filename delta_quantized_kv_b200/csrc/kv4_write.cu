@@ -9,10 +9,11 @@
 // steps.  A V word gathers one channel of each of 8 lanes (see
 // kv4_common.cuh): an 8 x 8 transpose of nibbles in three shuffle steps.
 //
-// Measured on one B200: 21495 tokens of 8 heads (D 128, 16 bits) quantised in 45
-// us, bound by instruction issue (191 instructions for 256 values, 70 % of the
-// slots); 131072 tokens read as bf16 in 137 us, 5.0 TB/s in and out, bound by
-// DRAM.
+// Measured on one B200: 21491 tokens of 8 heads (D 128, 16 bits) quantised in 44
+// us: 196 instructions for 256 values in 72 % of the issue slots, 57 % of the
+// ALU's, 6.9 warps a scheduler; no unit is full, and fewer instructions a value
+// is what would help.  131072 tokens read as bf16 in 138 us, 5.0 TB/s in and out,
+// bound by DRAM.
 #include <cuda_runtime.h>
 
 #include <cstdint>
