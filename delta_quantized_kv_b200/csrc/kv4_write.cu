@@ -373,16 +373,23 @@ read_kernel(View v, void *K, void *V, int per_warp, int heads) {
     }
 }
 
-// A warp's share: one row of each of its lanes while such warps are fewer than
-// 2048, all heads of a token in longer calls, and of 2 or 4 tokens in long ones
-// (the token's place is found once for them).  us of an append / a read of N
-// tokens of 8 heads (D 128, bf16) with a row each, and all heads of 1, 2, 4 tokens:
-//   256: 2.9/2.6, 3.7/2.9, -, -        512: 3.8/3.7, 3.7/2.8, 5.7/4.1, -
-//  1024: 5.7/5.1, 4.3/3.5, 5.7/4.1, -  4096: 18.4/14.5, 9.4/6.3, 10.2/7.6, 11.9/8.4
-//  8192: -, 16.8/10.6, 16.4/10.4, 18.6/13.1
-// 16384: -, 31.9/19.7, 30.9/18.2, 31.3/18.6
-// 65536: -, 122/80.6, 117/71.9, 116/70.8
-// and of 8 heads of D 64 in fp32: 512: 2.9/2.9, 3.1/2.9; 1024: 4.9/3.8, 3.4/3.4.
+// A warp's share: as many heads of a token as leave 2048 warps a tensor (a row of
+// each of its lanes, AHEAD of them, all), and 2 or 4 tokens in long calls (a
+// token's place is found once for its heads).  us of an append / a read, D 128,
+// bf16, with one row, AHEAD rows and all heads:
+//   8 heads,  256 tokens  2.9/2.6    3.7/2.9 (all)
+//             512         3.8/3.7    3.7/2.8
+//            1024         5.7/5.1    4.3/3.5
+//            4096        18.4/14.5   9.4/6.3
+//  32 heads,   64 tokens  3.1/2.9    3.7/3.1     8.4/5.3
+//             128         3.9/3.9    3.9/3.1     8.4/5.3
+//            1024        18.6/14.7   9.8/7.2    10.6/7.2
+//            2048        35.6/27.4  17.4/11.5   16.4/11.3
+// and of all 8 heads with 1, 2 and 4 tokens:
+//            4096 tokens  9.4/6.3   10.2/7.6    11.9/8.4
+//            8192        16.8/10.6  16.4/10.4   18.6/13.1
+//           16384        31.9/19.7  30.9/18.2   31.3/18.6
+//           65536       122/80.6   117/71.9    116/70.8
 struct Share {
     int tokens, heads;
     dim3 grid;
@@ -392,7 +399,8 @@ Share share_of(const View &v) {
     constexpr int RW = 32 / (L::D / 8);
     Share s;
     s.tokens = v.n_rows < 8192 ? 1 : v.n_rows < 16384 ? 2 : 4;
-    s.heads = (int64_t)v.n_rows * v.H < 2048 * RW ? RW : v.H;
+    s.heads = (int64_t)v.n_rows * v.H < 2048 * RW ? RW
+              : v.n_rows < 2048 && v.H > AHEAD * RW ? AHEAD * RW : v.H;
     const int64_t per = (int64_t)WARPS * s.tokens;
     s.grid = dim3((unsigned)((v.n_rows + per - 1) / per), 2, (v.H + s.heads - 1) / s.heads);
     return s;
