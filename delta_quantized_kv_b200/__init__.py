@@ -85,8 +85,9 @@ EXPORTS = ["dkv_abi_version", "dkv_cache_bytes", "dkv_cache_init", "dkv_encode",
            "dkv_append_decode_attn", "dkv_append_decode_attn_split",
            "dkv_append_decode_attn_merge", "dkv_lr_encode", "dkv_lr_decode_workspace_bytes",
            "dkv_lr_decode_attn", "dkv_debug_division_check", "dkv_kv4_page_bytes",
-           "dkv_kv4_init", "dkv_kv4_get_device_status", "dkv_kv4_append", "dkv_kv4_read", "dkv_kv4_decode_workspace_bytes",
-           "dkv_kv4_decode_attn", "dkv_kv4_prompt_workspace_bytes", "dkv_kv4_prompt_attn"]
+           "dkv_kv4_init", "dkv_kv4_get_device_status", "dkv_kv4_append", "dkv_kv4_read",
+           "dkv_kv4_decode_workspace_bytes", "dkv_kv4_decode_attn",
+           "dkv_kv4_prompt_workspace_bytes", "dkv_kv4_prompt_attn"]
 
 
 def load():

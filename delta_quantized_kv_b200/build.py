@@ -17,8 +17,8 @@ PKG = Path(__file__).resolve().parent
 CSRC = PKG / "csrc"
 OUT = PKG / "_lib" / "libdkv.so"
 OUT_CHECKED = PKG / "_lib" / "libdkv_checked.so"
-SOURCES = ["dkv_api.cu", "status.cu", "encode.cu", "decode.cu", "noalloc.cu", "lr_encode.cu", "lr_decode.cu",
-           "kv4_api.cu", "kv4_write.cu", "kv4_decode.cu", "kv4_prompt.cu"]
+SOURCES = ["dkv_api.cu", "status.cu", "encode.cu", "decode.cu", "noalloc.cu", "lr_encode.cu",
+           "lr_decode.cu", "kv4_api.cu", "kv4_write.cu", "kv4_decode.cu", "kv4_prompt.cu"]
 HEADERS = ["dkv_common.cuh", "dkv_internal.h", "kv4_common.cuh", "kv4_internal.h"]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared"]
