@@ -1237,13 +1237,11 @@ __global__ void __launch_bounds__(WARPS * 32, (QHL ? 2 : KCfg<FMT, MODE>::MINB))
     while (consumed < issued) {
         // ---- wait for the stage -------------------------------------------
         const uint8_t *st = mystages + stage_i * STAGE;
-        if (!mbar_wait_bounded(mybar + stage_i, (phase >> stage_i) & 1)) {
-            dead = true;
-            if (lane == 0) set_status(cv.header, DKV_DEV_TIMEOUT);
-        }
-        // a warp that gave up leaves the loop with this stage's copies (and any
-        // later ones) in flight; they are waited for below
+        if (!mbar_wait_bounded(mybar + stage_i, (phase >> stage_i) & 1)) dead = true;
+        // a warp that gave up (any of its lanes) leaves the loop with this stage's
+        // copies (and any later ones) in flight; they are waited for below
         dead = __any_sync(0xffffffffu, dead);
+        if (dead && lane == 0) set_status(cv.header, DKV_DEV_TIMEOUT);
         if (dead) break;
         phase ^= 1u << stage_i;
         const StageMeta meta = NS == 1 ? pend : mymeta[stage_i];

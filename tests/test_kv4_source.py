@@ -57,3 +57,12 @@ def test_the_runs_test_has_the_kernels_constants():
                  "const int64_t least = (int64_t)MIN_TILES * TN * G, n = total / least;",
                  "const int64_t each = (units - u.cost + tiles - 1) / tiles;"):
         assert line in s, line
+
+
+def test_a_split_warp_that_gives_up_says_so():
+    """Delta-KV's split kernel: any lane may run out of time first, so the report
+    comes behind the warp's vote and not from lane 0's own clock."""
+    s = code("decode.cu")
+    body = s[s.index("if (!mbar_wait_bounded("):]
+    body = body[:body.index("if (dead) break;")]
+    assert body.index("__any_sync(0xffffffffu, dead)") < body.index("set_status(cv.header, DKV_DEV_TIMEOUT)")
