@@ -28,9 +28,9 @@
 // are rounded to fp16 once; sums and scores are fp32.
 //
 // Measured on one B200: a prompt of 8192 tokens (32 heads over 8, D 128, bf16) in
-// 653 us a call, 840 TFLOP/s (calls queued behind one another: 610-622); chunks of
-// 500 and 160 tokens behind 24577 and 13187 positions in 278 us, 860 TFLOP/s
-// (259-261).  A CTA takes 4100-4500 clocks for two query tiles and 128 positions;
+// 653-660 us a call, 830-840 TFLOP/s (calls queued behind one another: 610-622);
+// chunks of 500 and 160 tokens behind 24577 and 13187 positions in 278-281 us,
+// 850-860 TFLOP/s (259-262).  A CTA takes 4100-4500 clocks for two query tiles and 128 positions;
 // the softmax warps are at work for 90 % of them, the tensor cores for 44 %; ALU
 // and exponentials are at 45 %, the issue slots at 55 %.
 #include <cuda_runtime.h>
